@@ -57,7 +57,8 @@ typedef enum {
   VLM_ERR_COUNT_MISMATCH = -4, /* device: placeholder count != number of image rows */
   VLM_ERR_TIMEOUT = -5,        /* device: a barrier wait exceeded its time budget */
   VLM_ERR_CUDA = -6,           /* a CUDA runtime call failed */
-  VLM_ERR_UNSUPPORTED = -7     /* shape the kernels do not implement (e.g. head_dim != 64) */
+  VLM_ERR_UNSUPPORTED = -7,    /* shape the kernels do not implement (e.g. head_dim != 64) */
+  VLM_ERR_BAD_PAGE = -8        /* device: a page table entry or a length outside the cache (vlm_kv4_*) */
 } vlm_status;
 
 /* Hyperparameters of the vision side. [K] Mistral3Model: vision_embed_dim
@@ -404,6 +405,131 @@ VLM_API int vlm_expand_placeholders(const int64_t* d_input_ids, int64_t n_ids, i
                                     void* d_workspace, size_t ws_bytes, int32_t* d_status, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The text side's attention, for the prompt that the scatter completes: causal
+ * attention over packed prompts with grouped heads, and a paged key/value
+ * cache held in 4 bits with the attention that reads it ([K] Mistral3Model:
+ * the text decoder's query heads share key heads; [P]: cache bytes per token).
+ * Rotary embedding and projections are the caller's. Inference only.
+ *
+ * 16-bit operands: dtype VLM_DTYPE_BF16 or VLM_DTYPE_F16 (vlm_kernels.h), rows
+ * [tokens][heads][head_dim], head_dim 64 or 128, heads of a token contiguous,
+ * the elements between tokens given as a stride (a multiple of 8, at least
+ * heads * head_dim), 16-byte aligned, so the column blocks of one projection's
+ * output can be passed as they are. heads is a multiple of kv_heads, at most
+ * 128 query heads per key head; query head h reads key head
+ * h / (heads / kv_heads). VLM_ERR_UNSUPPORTED otherwise.
+ *
+ * vlm_prompt_attention: sequence s has q_lens[s] queries and kv_lens[s] keys
+ *   (host arrays of n_seqs, >= 0, read during the call only); q and out hold
+ *   the sequences' queries one after the other, k and v their keys. The last
+ *   query sees every key, query i the keys j <= i + kv_len - q_len:
+ *     o_i = sum_j softmax_j(scale q_i . k_j) v_j.
+ *   kv_len > q_len is a prompt that goes on (its first keys from a cache); a
+ *   query that sees no key (kv_len < q_len) gives 0. Only the rows of the
+ *   listed queries are written. Keys and values that a row does not see do not
+ *   reach it, infinities and NaN included; a NaN logit makes its row NaN.
+ *   scale > 0. P is rounded to dtype, sums are fp32.
+ * ------------------------------------------------------------------------- */
+VLM_API int vlm_prompt_attention(int dtype, int heads, int kv_heads, int head_dim, const int32_t* q_lens,
+                                 const int32_t* kv_lens, int n_seqs, const void* d_q, int64_t q_stride,
+                                 const void* d_k, int64_t k_stride, const void* d_v, int64_t v_stride, float scale,
+                                 void* d_out, int64_t out_stride, int32_t* d_status, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The 4-bit cache. A pool of n_pages pages (16-byte aligned, page p at byte
+ * p * vlm_kv4_page_bytes); a page holds VLM_KV4_PAGE tokens of every key head,
+ * one head after the other, each as
+ *   key codes    [64][head_dim / 2]   E2M1, the even column in the low nibble
+ *   value codes  [64][head_dim / 2]
+ *   key scales   [64][head_dim / 16]  E4M3, one per 16 columns
+ *   value scales [64][head_dim / 16]
+ * (9/16 byte per value). A value is code * scale * k_sg or v_sg, the static
+ * global scales of keys and values (> 0): the NVFP4 format and recipe of
+ * vlm_quant_nvfp4; infinities saturate, a NaN in a block does not count for
+ * its scale and takes the largest code.
+ *
+ * d_table: device int32 [n_seqs][max_pages]: place j of sequence s is row
+ *   j % 64 of page d_table[s][j / 64]; entries behind a sequence's last page
+ *   are not read. Pages may be shared by sequences that only read them.
+ * Lengths and tables live on the device, so a captured graph replays with new
+ *   ones. An entry outside [0, n_pages) or a place outside the table sets
+ *   *d_status = VLM_ERR_BAD_PAGE; nothing outside the pool is touched, the
+ *   outputs of the sequences concerned are unspecified (written and read rows
+ *   without a page are skipped).
+ * n_seqs <= 65535.
+ *
+ * vlm_kv4_append: quantises new rows k, v (16-bit, strided) into the places
+ *   from d_lens[s] on (d_lens: tokens in the cache before; NULL: 0). Sequence
+ *   s has the rows [d_cu_new[s], d_cu_new[s + 1]) of k and v (device int32
+ *   [n_seqs + 1], from 0 to n_new, non-decreasing; NULL: one row each,
+ *   n_new == n_seqs). Lengths are the caller's to advance.
+ * vlm_kv4_read: the inverse: rows d_k, d_v [n_rows, kv_heads, head_dim] from
+ *   the places d_start[s] on (NULL: 0), rows of sequence s
+ *   [d_cu[s], d_cu[s + 1]); fp32(code * scale * global scale) rounded to dtype.
+ * ------------------------------------------------------------------------- */
+#define VLM_KV4_PAGE 64
+typedef struct {
+  void* d_pages;
+  int64_t n_pages;
+  int32_t kv_heads, head_dim;
+  float k_sg, v_sg;
+} vlm_kv4_cache;
+/* Bytes of one page; 0 for a head_dim other than 64 and 128 or kv_heads < 1. */
+VLM_API size_t vlm_kv4_page_bytes(int kv_heads, int head_dim);
+VLM_API int vlm_kv4_append(const vlm_kv4_cache* cache, const int32_t* d_table, int max_pages, int n_seqs,
+                           const int32_t* d_lens, const int32_t* d_cu_new, int64_t n_new, int dtype,
+                           const void* d_k, int64_t k_stride, const void* d_v, int64_t v_stride, int32_t* d_status,
+                           void* stream);
+VLM_API int vlm_kv4_read(const vlm_kv4_cache* cache, const int32_t* d_table, int max_pages, int n_seqs,
+                         const int32_t* d_start, const int32_t* d_cu, int64_t n_rows, int dtype, void* d_k, void* d_v,
+                         int32_t* d_status, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * vlm_kv4_attention -- attention of each sequence's last q_len tokens (1 when
+ * decoding; more to verify drafted tokens) over its cache.
+ *
+ * d_lens: device int32 [n_seqs], tokens in the cache, the new ones included.
+ *   New token i sits at place len - q_len + i and sees the places up to its
+ *   own; without any (len 0, or a place before 0) its row is 0.
+ * d_q: [n_seqs * q_len] rows of heads * head_dim, strided by q_stride;
+ * d_out: the same rows, contiguous, in dtype. q_len * (heads / kv_heads) at
+ *   most 65535 (VLM_ERR_BAD_SHAPE).
+ * d_weights: NULL, or device fp32 [n_seqs][kv_heads][max_pages * 64]:
+ *   weights[s][h][j] += the softmax weights of place j summed over the q_len
+ *   tokens and the query heads of key head h, for j < len; without atomics,
+ *   in a fixed order. Must not overlap any other buffer of the call.
+ * d_workspace: 256-byte aligned, vlm_kv4_attention_workspace_size bytes.
+ *
+ * vlm_kv4_evict -- keeps at most `budget` places of every (sequence, key
+ * head): all if len <= budget; else the first `sinks`, the last `recent`
+ * (sinks + recent <= budget) and of the others those with the largest weights
+ * (among equals the lower place; -0 equals 0, a NaN is below every number).
+ *   The kept rows move bit for bit, in order of place, to the places 0, 1, ...
+ *   behind d_to_table (int32 [n_seqs][to_max_pages], budget <= 64 *
+ *   to_max_pages), whose pages must be named once and be none of the
+ *   sequences' pages up to their lengths; otherwise, as for an entry outside
+ *   the pool, no page is written and *d_status = VLM_ERR_BAD_PAGE. Rows behind
+ *   the last kept one stay as they were. The old pages are then free.
+ * d_to_lens: int32 [n_seqs] = min(len, budget).
+ * d_to_weights: fp32 [n_seqs][kv_heads][to_max_pages * 64]: the kept places'
+ *   weights, 0 behind them.
+ * d_kept: NULL, or int32 [n_seqs][kv_heads][budget]: the kept places, -1
+ *   behind them.
+ * The results must not overlap d_lens and d_weights (VLM_ERR_INVALID_ARG).
+ * d_workspace: 256-byte aligned, vlm_kv4_evict_workspace_size bytes.
+ * ------------------------------------------------------------------------- */
+VLM_API size_t vlm_kv4_attention_workspace_size(int n_seqs, int heads, int kv_heads, int head_dim, int q_len);
+VLM_API int vlm_kv4_attention(const vlm_kv4_cache* cache, const int32_t* d_table, int max_pages, int n_seqs,
+                              const int32_t* d_lens, int dtype, int heads, int q_len, const void* d_q,
+                              int64_t q_stride, float scale, void* d_out, float* d_weights, void* d_workspace,
+                              size_t ws_bytes, int32_t* d_status, void* stream);
+VLM_API size_t vlm_kv4_evict_workspace_size(int64_t n_pages, int n_seqs, int kv_heads, int budget);
+VLM_API int vlm_kv4_evict(const vlm_kv4_cache* cache, const int32_t* d_table, int max_pages, int n_seqs,
+                          const int32_t* d_lens, const float* d_weights, int budget, int sinks, int recent,
+                          const int32_t* d_to_table, int to_max_pages, int32_t* d_to_lens, float* d_to_weights,
+                          int32_t* d_kept, void* d_workspace, size_t ws_bytes, int32_t* d_status, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Instrumentation (host-side, not thread-safe)
  * ------------------------------------------------------------------------- */
 /* Total kernels this library has launched in the process. */
@@ -412,7 +538,8 @@ VLM_API int64_t vlm_launch_count(void);
 VLM_API int vlm_profile_enable(int on);
 /* Kernel classes: 0 GEMM, 1 attention, 2 RMSNorm, 3 patch gather, 4 merge
  * gather, 5 scatter, 6 index setup, 7 weight packing, 8 image resize,
- * 9 placeholder expansion. Synchronises on the last
+ * 9 placeholder expansion, 10 prompt attention, 11 cache write and read,
+ * 12 cache attention, 13 cache eviction. Synchronises on the last
  * recorded event, then returns the launches and summed device milliseconds
  * recorded for `kclass` since profiling was enabled. */
 VLM_API int vlm_profile_query(int kclass, int64_t* launches, double* total_ms);

@@ -116,8 +116,9 @@ VLM_API int vlm_rmsnorm_fp8(float* d_x, const float* d_g0, const float* d_g1, vo
  * Returns 0 for a K that is not a positive multiple of 64 or rows < 1. */
 VLM_API size_t vlm_nvfp4_sf_bytes(int64_t rows, int64_t K);
 
-/* Element types of vlm_amax_scale and vlm_quant_nvfp4 inputs. */
-enum { VLM_DTYPE_BF16 = 0, VLM_DTYPE_F32 = 1 };
+/* Element types: bf16 and fp32 of vlm_amax_scale and vlm_quant_nvfp4 inputs,
+ * bf16 and fp16 of the text side's attention (vlm.h). */
+enum { VLM_DTYPE_BF16 = 0, VLM_DTYPE_F32 = 1, VLM_DTYPE_F16 = 2 };
 
 /* d_out[0] = fp32(max |x| / divisor) over n values of d_x (dtype VLM_DTYPE_BF16
  * or VLM_DTYPE_F32, device memory). With divisor 2688 (= 6 * 448) this is an

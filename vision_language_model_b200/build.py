@@ -22,7 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libvlm_b200.so")
 DEBUG_LIB = os.path.join(PKG, "libvlm_b200_debug.so")
 SOURCES = ["api.cu", "gemm_tcgen05.cu", "attention_tc.cu", "small_kernels.cu", "scatter_noalloc.cu", "frontend.cu",
-           "nvfp4.cu"]
+           "nvfp4.cu", "text_api.cu", "prompt_attention.cu", "kv4.cu", "kv4_attention.cu", "kv4_evict.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -430,6 +430,7 @@ const char* vlm_status_string(int status) {
     case VLM_ERR_TIMEOUT: return "VLM_ERR_TIMEOUT";
     case VLM_ERR_CUDA: return "VLM_ERR_CUDA";
     case VLM_ERR_UNSUPPORTED: return "VLM_ERR_UNSUPPORTED";
+    case VLM_ERR_BAD_PAGE: return "VLM_ERR_BAD_PAGE";
     default: return "VLM_ERR_UNKNOWN";
   }
 }

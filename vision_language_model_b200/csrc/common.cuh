@@ -21,7 +21,8 @@ namespace vlm {
 // ---------------------------------------------------------------------------
 enum KernelClass : int {
   KC_GEMM = 0, KC_ATTN = 1, KC_NORM = 2, KC_IM2COL = 3, KC_MERGE = 4,
-  KC_SCATTER = 5, KC_SETUP = 6, KC_PACK = 7, KC_FRONT = 8, KC_EXPAND = 9, KC_COUNT = 10
+  KC_SCATTER = 5, KC_SETUP = 6, KC_PACK = 7, KC_FRONT = 8, KC_EXPAND = 9, KC_PROMPT_ATTN = 10, KC_KV4_ROWS = 11,
+  KC_KV4_ATTN = 12, KC_KV4_EVICT = 13, KC_COUNT = 14
 };
 // Called around every launch: counts launches and, when profiling is on,
 // records a CUDA event pair on the launch stream.

@@ -115,6 +115,9 @@ int launch_wait_timeout_selftest(long long budget_cycles, int32_t* status, cudaS
 // 2D tensor map (bf16 or fp32 elements), 128-byte swizzle, box box_outer x box_inner.
 bool make_tmap_2d(CUtensorMap* map, const void* ptr, bool fp32, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                   uint32_t box_inner, uint32_t box_outer);
+// 3D bf16 or fp16 tensor map, 128-byte swizzle; strides (bytes) of the two outer dimensions.
+bool make_tmap_3d_16(CUtensorMap* map, bool half, const void* ptr, const uint64_t (&dims)[3],
+                     const uint64_t (&strides)[2], const uint32_t (&box)[3]);
 // 2D bf16 tensor map, 128-byte swizzle, box box_outer x box_inner (box_inner * 2 == 128 bytes).
 bool make_tmap_2d_bf16(CUtensorMap* map, const void* ptr, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                        uint32_t box_inner, uint32_t box_outer);

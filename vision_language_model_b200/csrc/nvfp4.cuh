@@ -38,6 +38,22 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
   return r;
 }
 
+// Eight E2M1 codes (one word, lowest nibble first) -> four pairs of fp16, exact.
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+// Two E4M3 bytes (the low 16 bits) -> a pair of fp16, exact.
+__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t bytes) {
+  uint32_t h2;
+  const uint16_t b = static_cast<uint16_t>(bytes);
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(b));
+  return h2;
+}
+
 // One block of 16 fp32 values with global scale sg (six_sg = fp32(6 sg)):
 // returns the E4M3 block scale byte s_b = e4m3(amax / six_sg) and sets the
 // 8 bytes of E2M1 codes e2m1(v * fp32(1 / fp32(s_b sg))) (all 0 when s_b is 0).

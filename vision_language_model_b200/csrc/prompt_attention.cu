@@ -1,0 +1,583 @@
+// Causal attention of packed prompts with grouped heads on the sm_100a tensor
+// cores, head dimension 64 or 128, bf16 or fp16. Sequence s has q_len queries
+// and kv_len keys; its last query sees every key:
+//   o_i = sum_{j <= i + kv_len - q_len} softmax_j(scale q_i . k_j) v_j,
+// query head h reads key head h / (heads / kv_heads).
+//
+// One work item = 2 row tiles of one sequence and one key head. A row tile
+// holds TPT = 128 / G consecutive tokens times the G query heads of the group
+// (row = token * G + head), so both tiles, 2 TPT tokens, share every key and
+// value tile that is loaded, and a short prompt still fills its rows. CTAs
+// (one per SM, 512 TMEM columns) take items blockIdx.x, + grid, ...; the
+// longest sequences and their last tiles come first. 18 warps:
+//   warp 0       TMA: both Q tiles, then K and V tiles of 128 keys into two
+//                2-stage rings (128-byte swizzle, 64-column boxes).
+//   warp 1       one thread issues, per key tile j and row tile t in turn,
+//                  S_t  = Q_t K_j^T           (tcgen05.mma kind::f16, M = N = 128)
+//                  O_t += P_t V_{j-1}         (A = P in TMEM, V in smem, MN-major)
+//                so while one row tile's product runs, the other's softmax does.
+//   warps 2..17  softmax, two threads per row (keys [0, 64) and [64, 128) of
+//                the tile), 256 threads per row tile: running maximum (moved
+//                only when it grows by more than 8 in log2 units), P as 16-bit
+//                pairs in TMEM, fp32 sums, O rescaled in TMEM when the maximum
+//                moved, and O / l at the end.
+// TMEM, D = 128: one S buffer that the row tiles take in turn [0, 128), P
+// [128, 192) and [192, 256), O [256, 384) and [384, 512); a tile's logits leave
+// S for registers at once, so the buffer is free again while its softmax runs.
+// D = 64: S [0, 128) and [128, 256), P [256, 384), O [384, 512).
+//
+// Roundings: P to the inputs' type (half a step; P <= 2^8 and its fp32 sum is
+// taken before rounding), the output once; everything else is fp32.
+// Places that a row does not see get weight 0. A weight of 0 does not stop an
+// infinity or NaN in V, so on key tiles that some row does not see in full the
+// softmax threads look V over in shared memory before the product: rows behind
+// the sequence's keys become 0, and a value that is not finite is replaced by 0
+// and its key noted; at the end rows that do see a noted key add its values.
+// A query that sees no key (kv_len < q_len) gives 0.
+#include <algorithm>
+#include <numeric>
+#include <vector>
+
+#include "softmax.cuh"
+#include "text_attention.cuh"
+
+namespace vlm {
+
+namespace {
+
+constexpr int BK = 128;        // keys per tile
+constexpr int kRows = 128;     // rows per row tile
+constexpr int HK = BK / 2;     // keys per softmax thread
+constexpr int kSoftWarps = 16;
+constexpr int kThreads = 32 * (2 + kSoftWarps);
+constexpr int kStages = 2;
+constexpr int kMaxSeqs = 256;  // sequences per launch (their table is a kernel argument)
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+
+struct SeqTable {
+  int n;
+  int off[kMaxSeqs + 1];  // work items before each sequence
+  int q0[kMaxSeqs], k0[kMaxSeqs], q_len[kMaxSeqs], kv_len[kMaxSeqs];
+};
+
+struct Args {
+  SeqTable t;
+  int kv_heads, group, tpt;
+  float sl2;  // scale * log2(e)
+  const void* v;
+  int64_t v_stride;
+  void* out;
+  int64_t out_stride;
+  int32_t* status;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int kSub = 128 * 128;           // bytes of 128 rows x 64 columns
+  static constexpr int kTile = kSub * (D / 64);    // one Q, K or V tile
+  static constexpr int kQ = 0, kK = 2 * kTile, kV = kK + kStages * kTile;
+  static constexpr int kBars = kV + kStages * kTile;
+  static constexpr int kXch = kBars + 256;         // row maxima [tile][parity][half][row], sums [tile][half][row]
+  static constexpr int kFlags = kXch + (8 + 4) * kRows * 4;  // noted keys, two sets of 512 bits
+  static constexpr int kSmem = kFlags + 2 * 64 + 1024;
+  static constexpr uint32_t s_col(int t) { return D == 128 ? 0 : 128 * t; }
+  static constexpr uint32_t p_col(int t) { return D == 128 ? 128 + 64 * t : 256 + 64 * t; }
+  static constexpr uint32_t o_col(int t) { return D == 128 ? 256 + 128 * t : 384 + 64 * t; }
+};
+
+template <typename T>
+constexpr bool is_half = std::is_same_v<T, __half>;
+
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc16(int m, int n, bool b_mn_major = false) {
+  return idesc_bf16(m, n, b_mn_major) & (is_half<T> ? ~((1u << 7) | (1u << 10)) : ~0u);  // format 0: fp16
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// A work item: sequence, key head, the row tiles' first tokens and key tiles.
+struct Item {
+  int q0, k0, q_len, kv_len, head, tok0;
+  int n[2];    // key tiles of each row tile
+  int shift;   // kv_len - q_len
+  __device__ __forceinline__ int tok(int t, int tpt) const { return tok0 + t * tpt; }
+};
+__device__ __forceinline__ Item item_of(const Args& a, int idx) {
+  int lo = 0, hi = a.t.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.t.off[mid] <= idx) lo = mid; else hi = mid - 1;
+  }
+  Item it;
+  it.q0 = a.t.q0[lo];
+  it.k0 = a.t.k0[lo];
+  it.q_len = a.t.q_len[lo];
+  it.kv_len = a.t.kv_len[lo];
+  const int r = idx - a.t.off[lo], tiles = (a.t.off[lo + 1] - a.t.off[lo]) / a.kv_heads;
+  it.head = r % a.kv_heads;
+  it.tok0 = (tiles - 1 - r / a.kv_heads) * 2 * a.tpt;
+  it.shift = it.kv_len - it.q_len;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int first = it.tok(t, a.tpt), last = min(it.q_len, first + a.tpt) - 1;
+    it.n[t] = first < it.q_len ? max(0, (it.shift + last + 1 + BK - 1) / BK) : 0;
+  }
+  return it;
+}
+
+template <typename T>
+__device__ __forceinline__ bool finite16(uint32_t w) {
+  constexpr uint32_t m = is_half<T> ? 0x7C007C00u : 0x7F807F80u;
+  return __vcmpeq2(w & m, m) == 0;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Args args, int n_items) {
+  using C = Cfg<D>;
+  constexpr bool kHalf = is_half<T>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
+  uint64_t* q_full = bars;
+  uint64_t* q_empty = bars + 1;
+  uint64_t* k_full = bars + 2;
+  uint64_t* k_empty = k_full + kStages;
+  uint64_t* v_full = k_empty + kStages;
+  uint64_t* v_empty = v_full + kStages;
+  uint64_t* s_full = v_empty + kStages;  // [2] row tiles
+  uint64_t* s_free = s_full + 2;         // [2] S buffers
+  uint64_t* p_full = s_free + 2;         // [2]
+  uint64_t* o_done = p_full + 2;         // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 2);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  uint32_t* flags = reinterpret_cast<uint32_t*>(smem + C::kFlags);  // [2][16]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(q_full), 1);
+    mbar_init(smem_u32(q_empty), 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(k_full + s), 1);
+      mbar_init(smem_u32(k_empty + s), 1);
+      mbar_init(smem_u32(v_full + s), 1);
+      mbar_init(smem_u32(v_empty + s), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(s_full + t), 1);
+      mbar_init(smem_u32(s_free + t), 256);
+      mbar_init(smem_u32(p_full + t), 256);
+      mbar_init(smem_u32(o_done + t), 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x < 32) flags[threadIdx.x] = 0;
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  volatile int* abort_v = abort_flag;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t q_bytes = 128u * args.group * args.tpt * (D / 64);
+      uint32_t kc = 0, vc = 0, qc = 0;
+      bool ok = true;
+      for (int idx = blockIdx.x; ok && idx < n_items; idx += gridDim.x) {
+        const Item it = item_of(args, idx);
+        const int n = max(it.n[0], it.n[1]);
+        if (n == 0) continue;
+        if (!mbar_wait(smem_u32(q_empty), (qc & 1) ^ 1, abort_v, args.status)) break;
+        const uint32_t qb = smem_u32(q_full);
+        mbar_arrive_expect_tx(qb, q_bytes * (it.n[1] > 0 ? 2 : 1));
+        for (int t = 0; t < (it.n[1] > 0 ? 2 : 1); ++t)
+          for (int x = 0; x < D / 64; ++x)
+            tma_load_3d(smem_u32(smem + C::kQ + t * C::kTile + x * C::kSub), &tm_q, qb, 64 * x, it.head * args.group,
+                        it.q0 + it.tok(t, args.tpt));
+        ++qc;
+        for (int j = 0; j <= n; ++j) {
+          if (j < n) {
+            const uint32_t st = kc % kStages;
+            if (!(ok = mbar_wait(smem_u32(k_empty + st), ((kc / kStages) & 1) ^ 1, abort_v, args.status))) break;
+            const uint32_t fb = smem_u32(k_full + st);
+            mbar_arrive_expect_tx(fb, C::kTile);
+            for (int x = 0; x < D / 64; ++x)
+              tma_load_3d(smem_u32(smem + C::kK + st * C::kTile + x * C::kSub), &tm_k, fb, 64 * x, it.head,
+                          it.k0 + j * BK);
+            ++kc;
+          }
+          if (j > 0) {
+            const uint32_t st = vc % kStages;
+            if (!(ok = mbar_wait(smem_u32(v_empty + st), ((vc / kStages) & 1) ^ 1, abort_v, args.status))) break;
+            const uint32_t fb = smem_u32(v_full + st);
+            mbar_arrive_expect_tx(fb, C::kTile);
+            for (int x = 0; x < D / 64; ++x)
+              tma_load_3d(smem_u32(smem + C::kV + st * C::kTile + x * C::kSub), &tm_v, fb, 64 * x, it.head,
+                          it.k0 + (j - 1) * BK);
+            ++vc;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc16<T>(kRows, BK);
+      constexpr uint32_t idesc_o = idesc16<T>(kRows, D, /*b_mn_major=*/true);
+      uint32_t kc = 0, vc = 0, qc = 0;
+      uint32_t sc[2] = {0, 0}, pc[2] = {0, 0};  // S tiles per buffer and P tiles per row tile so far
+      bool ok = true;
+      for (int idx = blockIdx.x; ok && idx < n_items; idx += gridDim.x) {
+        const Item it = item_of(args, idx);
+        const int n = max(it.n[0], it.n[1]);
+        if (n == 0) continue;
+        if (!mbar_wait(smem_u32(q_full), qc & 1, abort_v, args.status)) break;
+        for (int j = 0; ok && j <= n; ++j) {
+          const uint32_t ks = kc % kStages, vs = vc % kStages;
+          if (j < n && !(ok = mbar_wait(smem_u32(k_full + ks), (kc / kStages) & 1, abort_v, args.status))) break;
+          bool v_ready = false;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (j < it.n[t]) {
+              // the buffer's last logits have left for registers
+              const int b = D == 128 ? 0 : t;
+              if (sc[b] > 0 && !(ok = mbar_wait(smem_u32(s_free + b), (sc[b] - 1) & 1, abort_v, args.status))) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k / 4) * C::kSub;
+                umma_bf16_ss(tmem + C::s_col(t), smem_desc_sw128(smem_u32(smem + C::kQ + t * C::kTile + off)) + 2 * (k % 4),
+                             smem_desc_sw128(smem_u32(smem + C::kK + ks * C::kTile + off)) + 2 * (k % 4), idesc_s,
+                             k > 0 ? 1u : 0u);
+              }
+              umma_commit(smem_u32(s_full + t));
+              ++sc[b];
+            }
+            // the last user of this K tile: row tile 1, or 0 where 1 has fewer tiles
+            if (j < n && t == 1) umma_commit(smem_u32(k_empty + ks));
+            if (j == n - 1 && t == 1) umma_commit(smem_u32(q_empty));
+            if (j > 0 && j <= it.n[t]) {
+              // P is written by the threads that read O at the end of an item, after they did
+              if (!(ok = mbar_wait(smem_u32(p_full + t), pc[t] & 1, abort_v, args.status))) break;
+              if (!v_ready && !(ok = mbar_wait(smem_u32(v_full + vs), (vc / kStages) & 1, abort_v, args.status))) break;
+              v_ready = true;
+              tc_fence_after();
+              const uint64_t vdesc = smem_desc_sw128(smem_u32(smem + C::kV + vs * C::kTile), 1024, C::kSub);
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk)  // 16 keys: 8 TMEM columns of pairs, 2048 bytes of V
+                umma_bf16_ts(tmem + C::o_col(t), tmem + C::p_col(t) + 8 * kk, vdesc + 128 * kk, idesc_o,
+                             (j > 1 || kk > 0) ? 1u : 0u);
+              umma_commit(smem_u32(o_done + t));
+              ++pc[t];
+            }
+            if (j > 0 && t == 1) umma_commit(smem_u32(v_empty + vs));
+          }
+          if (j < n) ++kc;
+          if (j > 0) ++vc;
+        }
+        ++qc;
+      }
+    }
+  } else {
+    const int t = (warp - 2) >> 3, hf = ((warp - 2) >> 2) & 1, quad = warp & 3;
+    const int r = quad * 32 + lane;            // row of the tile = TMEM lane
+    const int pair_id = 1 + t * 4 + quad;      // named barrier of the two warps of these rows
+    const int tid = (warp - 2 - 8 * t) * 32 + lane;  // 0..255 in the row tile's threads
+    const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    float* xmax = reinterpret_cast<float*>(smem + C::kXch) + t * 4 * kRows;
+    float* xsum = reinterpret_cast<float*>(smem + C::kXch) + 8 * kRows + t * 2 * kRows;
+    const uint64_t sl2x2 = pair_f32(args.sl2);
+    const int row_tok = r / args.group, row_head = r - row_tok * args.group;
+    uint32_t sc = 0, oc = 0, vc_item = 0, items = 0;
+    bool ok = true;
+    // A warp whose wait failed keeps meeting the others at the named barriers,
+    // doing nothing else, so that none of them waits for it.
+    for (int idx = blockIdx.x; idx < n_items; idx += gridDim.x, ++items) {
+      const Item it = item_of(args, idx);
+      const int tok = it.tok(t, args.tpt) + row_tok;
+      const bool live = tok < it.q_len && row_tok < args.tpt;
+      const int lim = it.shift + tok + 1;                     // the row sees keys [0, lim)
+      const int lim_min = it.shift + it.tok(t, args.tpt) + 1;  // what every row of the tile sees
+      const int flag_base = max(0, it.shift + it.tok0 + 1) / BK * BK;
+      uint32_t* flag = flags + 16 * (items & 1);
+      // everyone has left the item before last, whose notes shared this set's twin
+      bar_sync(9, kSoftWarps * 32);
+      if (t == 0 && tid < 16) flags[16 * ((items & 1) ^ 1) + tid] = 0;
+      const int n = it.n[t], n_max = max(it.n[0], it.n[1]);
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j) {
+        if (ok) ok = mbar_wait_warp(smem_u32(s_full + t), sc & 1, abort_v, args.status);
+        ++sc;
+        if (!ok) {
+          bar_sync(pair_id, 64);
+          continue;
+        }
+        tc_fence_after();
+        uint32_t u[HK];
+        tmem_ld64(trow + C::s_col(t) + HK * hf, u);
+        tc_fence_before();
+        mbar_arrive(smem_u32(s_free + (D == 128 ? 0 : t)));
+        const bool masked = (j + 1) * BK > lim_min;
+        if (masked) {
+          const int nvalid = lim - j * BK - HK * hf;
+#pragma unroll
+          for (int c = 0; c < HK; ++c)
+            if (c >= nvalid) u[c] = __float_as_uint(-INFINITY);
+        }
+        const float m_own = row_max<true>(u) * args.sl2;
+        xmax[((j & 1) * 2 + hf) * kRows + r] = m_own;
+        bar_sync(pair_id, 64);
+        const float m_cand = fmaxf(m_own, xmax[((j & 1) * 2 + (hf ^ 1)) * kRows + r]);
+        const bool grow = m_cand > m + kRescaleThreshold;
+        const float m_new = grow ? m_cand : m;
+        const float corr = grow ? ex2(m - m_new) : 1.0f;
+        const bool any_grow = __any_sync(0xffffffffu, grow);
+        m = m_new;
+        const float ref = m == -INFINITY ? 0.0f : m;
+        uint32_t pk[HK / 2];
+        const float sum = masked ? row_exp<false, kHalf>(u, sl2x2, ref, pk) : row_exp<true, kHalf>(u, sl2x2, ref, pk);
+        l = l * corr + sum;
+        if (!(m_own < INFINITY)) l = NAN;  // a NaN or infinite logit: exp2_poly would swallow it
+        if (j > 0) {
+          // the product with the tile before must be done before O is rescaled and P overwritten
+          ok = mbar_wait_warp(smem_u32(o_done + t), (oc - 1) & 1, abort_v, args.status);
+          if (!ok) continue;
+          tc_fence_after();
+        }
+        tmem_st32(trow + C::p_col(t) + 32 * hf, pk);
+        if (j > 0 && any_grow) {
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x) {
+            const uint32_t col = trow + C::o_col(t) + (D / 2) * hf + 32 * x;
+            uint32_t o[32];
+            tmem_ld32(col, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+            tmem_st32(col, o);
+          }
+        }
+        if (masked && (t == 0 || j >= it.n[0])) {
+          // look this V tile over before its first product
+          const uint32_t vc = vc_item + j, vs = vc % kStages;
+          ok = mbar_wait_warp(smem_u32(v_full + vs), (vc / kStages) & 1, abort_v, args.status);
+          if (ok) {
+            const int valid = it.kv_len - j * BK;
+            for (int x = tid; x < BK * D / 8; x += 256) {
+              const int sub = x / (BK * 8), row = (x >> 3) % BK, ch = x & 7;
+              uint4* at = reinterpret_cast<uint4*>(smem + C::kV + vs * C::kTile + sub * C::kSub + row * 128 +
+                                                   ((ch ^ (row & 7)) << 4));
+              if (row >= valid) {
+                *at = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              uint4 w = *at;
+              if (finite16<T>(w.x) && finite16<T>(w.y) && finite16<T>(w.z) && finite16<T>(w.w)) continue;
+              constexpr uint32_t e = kHalf ? 0x7C007C00u : 0x7F807F80u;
+              w.x &= ~__vcmpeq2(w.x & e, e);
+              w.y &= ~__vcmpeq2(w.y & e, e);
+              w.z &= ~__vcmpeq2(w.z & e, e);
+              w.w &= ~__vcmpeq2(w.w & e, e);
+              *at = w;
+              const int key = j * BK + row - flag_base;
+              if (key >= 0 && key < 512) atomicOr(flag + (key >> 5), 1u << (key & 31));
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(p_full + t));
+        ++oc;
+      }
+      xsum[hf * kRows + r] = l;
+      bar_sync(pair_id, 64);
+      l += xsum[(hf ^ 1) * kRows + r];
+      if (ok && n > 0) ok = mbar_wait_warp(smem_u32(o_done + t), (oc - 1) & 1, abort_v, args.status);
+      if (ok) {
+        tc_fence_after();
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint32_t noted = 0;
+        if (n > 0)
+          for (int i = 0; i < 16; ++i) noted |= *reinterpret_cast<volatile uint32_t*>(flag + i);
+        T* dst = static_cast<T*>(args.out) + static_cast<int64_t>(it.q0 + tok) * args.out_stride +
+                 (it.head * args.group + row_head) * D + (D / 2) * hf;
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_ld32(trow + C::o_col(t) + (D / 2) * hf + 32 * x, o);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0;
+          }
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+            if (noted != 0) {
+              // keys whose values are not finite: rows that see them take those values
+              for (int key = 0; key < 512 && flag_base + key < lim; ++key) {
+                if (!((flag[key >> 5] >> (key & 31)) & 1)) continue;
+                const T* vr = static_cast<const T*>(args.v) + static_cast<int64_t>(it.k0 + flag_base + key) * args.v_stride +
+                              it.head * D + (D / 2) * hf + 32 * x;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float val = static_cast<float>(vr[i]);
+                  if (!(fabsf(val) < INFINITY)) o[i] = __float_as_uint(__uint_as_float(o[i]) + val);
+                }
+              }
+            }
+            uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack16<T>(__uint_as_float(o[8 * i + 2 * k]), __uint_as_float(o[8 * i + 2 * k + 1]));
+              d4[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      vc_item += n_max;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Opts the kernel in to its shared memory, once per device.
+template <typename T, int D>
+bool smem_ready() {
+  static bool done[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev < 64 && done[dev]) return true;
+  if (cudaFuncSetAttribute(prompt_attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem) !=
+      cudaSuccess)
+    return false;
+  if (dev < 64) done[dev] = true;
+  return true;
+}
+
+// Tensor map of 16-bit [tokens, heads, D] with `stride` elements between
+// tokens: 128-byte swizzle, box 64 columns x box_heads x box_tokens.
+bool tmap_3d(CUtensorMap* map, bool half, const void* ptr, int64_t tokens, int heads, int d, int64_t stride,
+             int box_heads, int box_tokens) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(heads), static_cast<uint64_t>(tokens)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(d) * 2, static_cast<uint64_t>(stride) * 2};
+  const uint32_t box[3] = {64, static_cast<uint32_t>(box_heads), static_cast<uint32_t>(box_tokens)};
+  return make_tmap_3d_16(map, half, ptr, dims, strides, box);
+}
+
+}  // namespace
+
+int launch_prompt_attention(const PromptAttn& p, cudaStream_t s) {
+  const int group = p.heads / p.kv_heads;
+  const bool half = p.dtype == VLM_DTYPE_F16;
+  int64_t total_q = 0, total_k = 0;
+  for (int i = 0; i < p.n_seqs; ++i) {
+    total_q += p.q_lens[i];
+    total_k += p.kv_lens[i];
+  }
+  if (total_q == 0) return VLM_OK;
+  CUtensorMap tq, tk, tv;
+  const int tpt = kRows / group;
+  // no key at all: the key and value maps are never used
+  if (!tmap_3d(&tq, half, p.q, total_q, p.heads, p.head_dim, p.q_stride, group, tpt)) return VLM_ERR_CUDA;
+  if (total_k > 0) {
+    if (!tmap_3d(&tk, half, p.k, total_k, p.kv_heads, p.head_dim, p.k_stride, 1, BK) ||
+        !tmap_3d(&tv, half, p.v, total_k, p.kv_heads, p.head_dim, p.v_stride, 1, BK))
+      return VLM_ERR_CUDA;
+  } else {
+    tk = tv = tq;
+  }
+  auto run = [&](auto kern, int smem, bool ready) -> int {
+    if (!ready) return VLM_ERR_CUDA;
+    // the longest sequences first: their items are the largest
+    std::vector<int> order(p.n_seqs);
+    std::iota(order.begin(), order.end(), 0);
+    std::vector<int> q0(p.n_seqs), k0(p.n_seqs);
+    for (int i = 0, q = 0, k = 0; i < p.n_seqs; ++i) {
+      q0[i] = q;
+      k0[i] = k;
+      q += p.q_lens[i];
+      k += p.kv_lens[i];
+    }
+    std::stable_sort(order.begin(), order.end(), [&](int x, int y) { return p.kv_lens[x] > p.kv_lens[y]; });
+    int launches = 0;
+    for (int first = 0; first < p.n_seqs; first += kMaxSeqs) {
+      Args a;
+      a.t.n = 0;
+      int64_t items = 0;
+      for (int i = first; i < std::min(p.n_seqs, first + kMaxSeqs); ++i) {
+        const int x = order[i];
+        if (p.q_lens[x] == 0) continue;
+        const int k = a.t.n++;
+        a.t.off[k] = static_cast<int>(items);
+        a.t.q0[k] = q0[x];
+        a.t.k0[k] = k0[x];
+        a.t.q_len[k] = p.q_lens[x];
+        a.t.kv_len[k] = p.kv_lens[x];
+        items += (static_cast<int64_t>(p.q_lens[x]) + 2 * tpt - 1) / (2 * tpt) * p.kv_heads;
+        if (items > 0x7FFFFFFF - 65536) return VLM_ERR_BAD_SHAPE;
+      }
+      if (a.t.n == 0) continue;
+      a.t.off[a.t.n] = static_cast<int>(items);
+      a.kv_heads = p.kv_heads;
+      a.group = group;
+      a.tpt = tpt;
+      a.sl2 = p.scale * 1.4426950408889634f;
+      a.v = p.v;
+      a.v_stride = p.v_stride;
+      a.out = p.out;
+      a.out_stride = p.out_stride;
+      a.status = p.status;
+      const int grid = static_cast<int>(std::min<int64_t>(items, num_sms()));
+      const cudaError_t e =
+          launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, tq, tk, tv, a, static_cast<int>(items));
+      if (e != cudaSuccess) return VLM_ERR_CUDA;
+      ++launches;
+    }
+    note_extra_launches(launches - 1);
+    return VLM_OK;
+  };
+  launch_begin(KC_PROMPT_ATTN, s);
+  int rc;
+  if (half)
+    rc = p.head_dim == 128 ? run(prompt_attn_kernel<__half, 128>, Cfg<128>::kSmem, smem_ready<__half, 128>())
+                           : run(prompt_attn_kernel<__half, 64>, Cfg<64>::kSmem, smem_ready<__half, 64>());
+  else
+    rc = p.head_dim == 128 ? run(prompt_attn_kernel<__nv_bfloat16, 128>, Cfg<128>::kSmem, smem_ready<__nv_bfloat16, 128>())
+                           : run(prompt_attn_kernel<__nv_bfloat16, 64>, Cfg<64>::kSmem, smem_ready<__nv_bfloat16, 64>());
+  launch_end(KC_PROMPT_ATTN, s);
+  return rc;
+}
+
+}  // namespace vlm

@@ -20,13 +20,13 @@ DEBUG_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvl
 _lib = None
 
 # vlm_status values (include/vlm.h)
-OK, ERR_INVALID_ARG, ERR_BAD_SHAPE, ERR_WORKSPACE, ERR_COUNT_MISMATCH, ERR_TIMEOUT, ERR_CUDA, ERR_UNSUPPORTED = \
-    0, -1, -2, -3, -4, -5, -6, -7
+OK, ERR_INVALID_ARG, ERR_BAD_SHAPE, ERR_WORKSPACE, ERR_COUNT_MISMATCH, ERR_TIMEOUT, ERR_CUDA, ERR_UNSUPPORTED, \
+    ERR_BAD_PAGE = 0, -1, -2, -3, -4, -5, -6, -7, -8
 # epilogues (include/vlm_kernels.h)
 EPI_BF16, EPI_F32, EPI_RESID, EPI_SWIGLU, EPI_ROPE, EPI_GELU = range(6)
 # profiling kernel classes
 KCLASS = {"gemm": 0, "attention": 1, "rmsnorm": 2, "im2col": 3, "merge": 4, "scatter": 5, "setup": 6, "pack": 7,
-          "resize": 8, "expand": 9}
+          "resize": 8, "expand": 9, "prompt_attention": 10, "kv4_rows": 11, "kv4_attention": 12, "kv4_evict": 13}
 
 
 class VlmError(RuntimeError):
@@ -43,6 +43,11 @@ class Config(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class Kv4CacheDesc(ctypes.Structure):
+    _fields_ = [("d_pages", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("k_sg", ctypes.c_float), ("v_sg", ctypes.c_float)]
 
 
 class TowerWeights(ctypes.Structure):
@@ -93,6 +98,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(_LIB_PATH)
         P, I32, I64, SZ, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
         CP = ctypes.POINTER(Config)
+        KP = ctypes.POINTER(Kv4CacheDesc)
         sig = {
             "vlm_status_string": (ctypes.c_char_p, [I32]),
             "vlm_status_sync": (I32, [P, P]),
@@ -133,6 +139,14 @@ def lib() -> ctypes.CDLL:
             "vlm_rmsnorm_nvfp4": (I32, [P, P, P, P, P, I64, I32, F, F, P]),
             "vlm_attention_nvfp4": (I32, [P, I64, I32, I32, P, I32, P, P, F, P, SZ, P, P]),
             "vlm_patch_embed": (I32, [CP, P, P, I32, P, P, P, SZ, P, P]),
+            "vlm_prompt_attention": (I32, [I32, I32, I32, I32, P, P, I32, P, I64, P, I64, P, I64, F, P, I64, P, P]),
+            "vlm_kv4_page_bytes": (SZ, [I32, I32]),
+            "vlm_kv4_append": (I32, [KP, P, I32, I32, P, P, I64, I32, P, I64, P, I64, P, P]),
+            "vlm_kv4_read": (I32, [KP, P, I32, I32, P, P, I64, I32, P, P, P, P]),
+            "vlm_kv4_attention_workspace_size": (SZ, [I32, I32, I32, I32, I32]),
+            "vlm_kv4_attention": (I32, [KP, P, I32, I32, P, I32, I32, I32, P, I64, F, P, P, P, SZ, P, P]),
+            "vlm_kv4_evict_workspace_size": (SZ, [I64, I32, I32, I32]),
+            "vlm_kv4_evict": (I32, [KP, P, I32, I32, P, P, I32, I32, I32, P, I32, P, P, P, P, SZ, P, P]),
             "vlm_launch_count": (I64, []),
             "vlm_profile_enable": (I32, [I32]),
             "vlm_profile_query": (I32, [I32, ctypes.POINTER(I64), ctypes.POINTER(ctypes.c_double)]),
@@ -706,6 +720,252 @@ def attention_nvfp4(qkv: torch.Tensor, cu_seqlens, heads: int, s_global: float, 
                                  ws.data_ptr(), ws.numel(), _dev(status, "status"), _stream(stream)),
            "vlm_attention_nvfp4")
     return q, sf
+
+
+# ---------------------------------------------------------------------------
+# The text side's attention: prompts and the paged 4-bit cache
+# ---------------------------------------------------------------------------
+DTYPE_F16 = 2
+KV4_PAGE = 64  # tokens per page (VLM_KV4_PAGE)
+_DTYPE16 = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+
+
+def _dtype16(dtype: torch.dtype) -> int:
+    code = _DTYPE16.get(dtype)
+    if code is None:
+        raise TypeError(f"bf16 or fp16 expected, got {dtype}")
+    return code
+
+
+def _rows16(t: torch.Tensor, name: str, like: torch.Tensor) -> tuple:
+    """(pointer, elements between tokens) of 16-bit [tokens, heads, head_dim] rows, heads contiguous."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.device != like.device or not t.is_cuda:
+        raise ValueError(f"{name} must be on the CUDA device of the other operands")
+    n, heads, dim = t.shape
+    if n and heads and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), t.stride(0) if n > 1 else heads * dim
+
+
+def _int32_dev(t: torch.Tensor | None, name: str, shape: tuple, dev: torch.device) -> int | None:
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    return _dev(t, name)
+
+
+class _on:
+    """Makes `dev` the current device for a call whose tensors live there."""
+
+    def __init__(self, dev: torch.device):
+        self.dev, self.old = dev.index, None
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        if self.dev is not None and cur != self.dev:
+            self.old = cur
+            torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        if self.old is not None:
+            torch.cuda.set_device(self.old)
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_lens, kv_lens=None,
+                     scale: float | None = None, out=None, status=None, stream=None) -> torch.Tensor:
+    """Causal attention of packed prompts with grouped heads (vlm_prompt_attention).
+
+    q [sum(q_lens), heads, head_dim], k and v [sum(kv_lens), kv_heads, head_dim]: bf16 or fp16, any
+    stride between tokens (column blocks of one projection's output). q_lens, kv_lens: host lists;
+    kv_lens None: the same. The last query of a sequence sees every key. scale None:
+    1 / sqrt(head_dim). Returns out [sum(q_lens), heads, head_dim]."""
+    q_lens = [int(n) for n in q_lens]
+    kv_lens = q_lens if kv_lens is None else [int(n) for n in kv_lens]
+    n = len(q_lens)
+    if len(kv_lens) != n:
+        raise ValueError("q_lens and kv_lens must list the same sequences")
+    dt = _dtype16(q.dtype)
+    qp, qs = _rows16(q, "q", q)
+    kp, ks = _rows16(k, "k", q)
+    vp, vs = _rows16(v, "v", q)
+    T, heads, dim = q.shape
+    if k.shape != v.shape or k.shape[2] != dim:
+        raise ValueError("k and v must have one shape and q's head_dim")
+    if sum(q_lens) != T or sum(kv_lens) != k.shape[0]:
+        raise ValueError(f"the lengths add up to {sum(q_lens)} and {sum(kv_lens)}, q has {T} rows and k {k.shape[0]}")
+    with _on(q.device):
+        if out is None:
+            out = _empty((T, heads, dim), dtype=q.dtype, device=q.device)
+        elif tuple(out.shape) != (T, heads, dim):
+            raise ValueError("out must have q's shape")
+        op, os_ = _rows16(out, "out", q)
+        if status is None:
+            status = new_status(q.device)
+        arr = ctypes.c_int32 * max(1, n)
+        _check(lib().vlm_prompt_attention(dt, heads, k.shape[1], dim, arr(*q_lens), arr(*kv_lens), n, qp, qs, kp, ks,
+                                          vp, vs, float(dim ** -0.5 if scale is None else scale), op, os_,
+                                          _dev(status, "status"), _stream(stream)), "vlm_prompt_attention")
+    return out
+
+
+def kv4_page_bytes(kv_heads: int, head_dim: int) -> int:
+    """Bytes of a page of the 4-bit cache (host only)."""
+    return int(lib().vlm_kv4_page_bytes(int(kv_heads), int(head_dim)))
+
+
+def kv4_pages(n_pages: int, kv_heads: int, head_dim: int, device="cuda") -> torch.Tensor:
+    """A pool of empty pages: uint8 [n_pages, kv_heads, bytes of one head's page]."""
+    nbytes = kv4_page_bytes(kv_heads, head_dim)
+    if nbytes == 0:
+        raise VlmError(ERR_UNSUPPORTED, "vlm_kv4_page_bytes")
+    return _zeros((n_pages, kv_heads, nbytes // kv_heads), dtype=torch.uint8, device=device)
+
+
+def _kv4(pages: torch.Tensor, table: torch.Tensor, k_sg: float, v_sg: float) -> tuple:
+    """(descriptor, table pointer, entries per row, sequences) of a cache and its page table."""
+    if pages.dtype != torch.uint8 or pages.dim() != 3 or pages.shape[2] not in (KV4_PAGE * 72, KV4_PAGE * 144):
+        raise ValueError("pages must be uint8 [n_pages, kv_heads, page bytes] as kv4_pages makes them")
+    if table.dim() != 2:
+        raise ValueError("table must be int32 [n_seqs, max_pages]")
+    tp = _int32_dev(table, "table", tuple(table.shape), pages.device)
+    desc = Kv4CacheDesc(_dev(pages, "pages"), pages.shape[0], pages.shape[1], pages.shape[2] // 72, k_sg, v_sg)
+    return ctypes.byref(desc), tp, table.shape[1], table.shape[0]
+
+
+def kv4_append(pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+               k_sg: float, v_sg: float, cu_new: torch.Tensor | None = None, status=None, stream=None) -> None:
+    """Quantises new rows k, v [n_new, kv_heads, head_dim] (bf16 or fp16) into the cache's places from
+    lens[s] on (vlm_kv4_append). table int32 [n_seqs, max_pages] and lens int32 [n_seqs] (None: 0) are
+    device tensors, as is cu_new int32 [n_seqs + 1], the rows of each sequence (None: one row each).
+    The global scales k_sg, v_sg are the cache's for good. lens is not advanced."""
+    desc, tp, width, n = _kv4(pages, table, k_sg, v_sg)
+    dev = pages.device
+    dt = _dtype16(k.dtype)
+    kp, ks = _rows16(k, "k", k)
+    vp, vs = _rows16(v, "v", k)
+    if k.device != dev or k.shape != v.shape or k.shape[1] != pages.shape[1] or k.shape[2] != pages.shape[2] // 72:
+        raise ValueError("k and v must be [n_new, kv_heads, head_dim] of the cache, on its device")
+    with _on(dev):
+        if status is None:
+            status = new_status(dev)
+        _check(lib().vlm_kv4_append(desc, tp, width, n, _int32_dev(lens, "lens", (n,), dev),
+                                    _int32_dev(cu_new, "cu_new", (n + 1,), dev), k.shape[0], dt, kp, ks, vp, vs,
+                                    _dev(status, "status"), _stream(stream)), "vlm_kv4_append")
+
+
+def kv4_read(pages: torch.Tensor, table: torch.Tensor, k_sg: float, v_sg: float, cu: torch.Tensor | None, n_rows: int,
+             start: torch.Tensor | None = None, dtype: torch.dtype = torch.bfloat16, k=None, v=None, status=None,
+             stream=None) -> tuple:
+    """Rows of the cache in 16 bits (vlm_kv4_read): k, v [n_rows, kv_heads, head_dim], the rows
+    [cu[s], cu[s + 1]) from sequence s's places start[s] on (None: 0; cu None: one row each)."""
+    desc, tp, width, n = _kv4(pages, table, k_sg, v_sg)
+    dev = pages.device
+    shape = (int(n_rows), pages.shape[1], pages.shape[2] // 72)
+    with _on(dev):
+        k = _empty(shape, dtype=dtype, device=dev) if k is None else k
+        v = _empty(shape, dtype=dtype, device=dev) if v is None else v
+        dt = _dtype16(k.dtype)
+        if tuple(k.shape) != shape or tuple(v.shape) != shape or v.dtype != k.dtype or k.device != dev \
+                or v.device != dev:
+            raise ValueError(f"k and v must be {list(shape)} of one type, on the cache's device")
+        if status is None:
+            status = new_status(dev)
+        _check(lib().vlm_kv4_read(desc, tp, width, n, _int32_dev(start, "start", (n,), dev),
+                                  _int32_dev(cu, "cu", (n + 1,), dev), int(n_rows), dt, _dev(k, "k"), _dev(v, "v"),
+                                  _dev(status, "status"), _stream(stream)), "vlm_kv4_read")
+    return k, v
+
+
+def kv4_attention_workspace_size(n_seqs: int, heads: int, kv_heads: int, head_dim: int, q_len: int = 1) -> int:
+    return int(lib().vlm_kv4_attention_workspace_size(int(n_seqs), int(heads), int(kv_heads), int(head_dim),
+                                                      int(q_len)))
+
+
+def kv4_attention(pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, q: torch.Tensor, k_sg: float,
+                  v_sg: float, scale: float | None = None, weights: torch.Tensor | None = None, out=None,
+                  workspace=None, status=None, stream=None) -> torch.Tensor:
+    """Attention of each sequence's last q_len = q.shape[0] / n_seqs tokens over its cache
+    (vlm_kv4_attention). q [n_seqs * q_len, heads, head_dim] bf16 or fp16; lens: device int32 [n_seqs],
+    the new tokens included. weights: fp32 [n_seqs, kv_heads, max_pages * 64], to which every place's
+    softmax weight is added, summed over the new tokens and the key head's query heads."""
+    desc, tp, width, n = _kv4(pages, table, k_sg, v_sg)
+    dev = pages.device
+    dt = _dtype16(q.dtype)
+    qp, qs = _rows16(q, "q", q)
+    T, heads, dim = q.shape
+    if q.device != dev or n == 0 or T == 0 or T % n != 0 or dim != pages.shape[2] // 72:
+        raise ValueError("q must be [n_seqs * q_len, heads, head_dim] of the cache, on its device")
+    kv_heads, m = pages.shape[1], T // n
+    if weights is not None and (weights.dtype != torch.float32 or weights.device != dev
+                                or tuple(weights.shape) != (n, kv_heads, width * KV4_PAGE)):
+        raise ValueError("weights must be fp32 [n_seqs, kv_heads, max_pages * 64]")
+    L = lib()
+    with _on(dev):
+        if out is None:
+            out = _empty((T, heads, dim), dtype=q.dtype, device=dev)
+        elif tuple(out.shape) != (T, heads, dim) or out.dtype != q.dtype or out.device != dev:
+            raise ValueError("out must have q's shape, type and device")
+        if workspace is None:
+            workspace = _empty(max(256, L.vlm_kv4_attention_workspace_size(n, heads, kv_heads, dim, m)),
+                               dtype=torch.uint8, device=dev)
+        if status is None:
+            status = new_status(dev)
+        _check(L.vlm_kv4_attention(desc, tp, width, n, _int32_dev(lens, "lens", (n,), dev), dt, heads, m, qp, qs,
+                                   float(dim ** -0.5 if scale is None else scale), _dev(out, "out"),
+                                   _dev(weights, "weights"), _dev(workspace, "workspace"), workspace.numel(),
+                                   _dev(status, "status"), _stream(stream)), "vlm_kv4_attention")
+    return out
+
+
+def kv4_evict_workspace_size(n_pages: int, n_seqs: int, kv_heads: int, budget: int) -> int:
+    return int(lib().vlm_kv4_evict_workspace_size(int(n_pages), int(n_seqs), int(kv_heads), int(budget)))
+
+
+def kv4_evict(pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, weights: torch.Tensor,
+              to_table: torch.Tensor, budget: int, sinks: int = 0, recent: int = 0, to_lens=None, kept=None,
+              to_weights=None, workspace=None, status=None, stream=None) -> tuple:
+    """Keeps at most `budget` places per (sequence, key head) -- the first `sinks`, the last `recent`,
+    and those with the largest summed weights -- and moves them to the fresh pages of to_table int32
+    [n_seqs, to_max_pages] (vlm_kv4_evict). Returns (to_lens int32 [n_seqs], kept int32
+    [n_seqs, kv_heads, budget], to_weights fp32 [n_seqs, kv_heads, to_max_pages * 64])."""
+    desc, tp, width, n = _kv4(pages, table, 1.0, 1.0)
+    dev, kv_heads, budget = pages.device, pages.shape[1], int(budget)
+    if weights.dtype != torch.float32 or weights.device != dev \
+            or tuple(weights.shape) != (n, kv_heads, width * KV4_PAGE):
+        raise ValueError("weights must be fp32 [n_seqs, kv_heads, max_pages * 64]")
+    if to_table.dim() != 2 or budget < 1:
+        raise ValueError("to_table must be int32 [n_seqs, to_max_pages] and budget at least 1")
+    to_width = to_table.shape[1]
+    ttp = _int32_dev(to_table, "to_table", (n, to_width), dev)
+    L = lib()
+    with _on(dev):
+        if to_lens is None:
+            to_lens = _empty(n, dtype=torch.int32, device=dev)
+        if kept is None:
+            kept = _empty((n, kv_heads, budget), dtype=torch.int32, device=dev)
+        if to_weights is None:
+            to_weights = _empty((n, kv_heads, to_width * KV4_PAGE), dtype=torch.float32, device=dev)
+        elif to_weights.dtype != torch.float32 or tuple(to_weights.shape) != (n, kv_heads, to_width * KV4_PAGE) \
+                or to_weights.device != dev:
+            raise ValueError("to_weights must be fp32 [n_seqs, kv_heads, to_max_pages * 64]")
+        if workspace is None:
+            workspace = _empty(max(256, L.vlm_kv4_evict_workspace_size(pages.shape[0], n, kv_heads, budget)),
+                               dtype=torch.uint8, device=dev)
+        if status is None:
+            status = new_status(dev)
+        _check(L.vlm_kv4_evict(desc, tp, width, n, _int32_dev(lens, "lens", (n,), dev), _dev(weights, "weights"),
+                               budget, int(sinks), int(recent), ttp, to_width,
+                               _int32_dev(to_lens, "to_lens", (n,), dev), _dev(to_weights, "to_weights"),
+                               _int32_dev(kept, "kept", (n, kv_heads, budget), dev), _dev(workspace, "workspace"),
+                               workspace.numel(), _dev(status, "status"), _stream(stream)), "vlm_kv4_evict")
+    return to_lens, kept, to_weights
 
 
 def rmsnorm(x: torch.Tensor, g1: torch.Tensor, g0=None, eps: float = 1e-5, out=None, stream=None) -> torch.Tensor:
