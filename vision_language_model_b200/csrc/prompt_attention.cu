@@ -8,19 +8,25 @@
 // holds TPT = 128 / G consecutive tokens times the G query heads of the group
 // (row = token * G + head), so both tiles, 2 TPT tokens, share every key and
 // value tile that is loaded, and a short prompt still fills its rows. CTAs
-// (one per SM, 512 TMEM columns) take items blockIdx.x, + grid, ...; the
-// longest sequences and their last tiles come first. 18 warps:
+// (one per SM, 512 TMEM columns) take items in turn, forwards and backwards
+// through the list; the longest sequences and their last tiles come first.
+// 20 warps:
 //   warp 0       TMA: both Q tiles, then K and V tiles of 128 keys into two
 //                2-stage rings (128-byte swizzle, 64-column boxes).
-//   warp 1       one thread issues, per key tile j and row tile t in turn,
+//   warps 1, 2   issue row tile t's products, one warp each, for key tile j
 //                  S_t  = Q_t K_j^T           (tcgen05.mma kind::f16, M = N = 128)
 //                  O_t += P_t V_{j-1}         (A = P in TMEM, V in smem, MN-major)
-//                so while one row tile's product runs, the other's softmax does.
-//   warps 2..17  softmax, two threads per row (keys [0, 64) and [64, 128) of
+//                Issuing an instruction costs about 90 cycles, the tensor core
+//                needs 64 for it: one warp for both tiles was the bound
+//                (3,520 cycles per key tile at D = 128).
+//   warps 4..19  softmax, two threads per row (keys [0, 64) and [64, 128) of
 //                the tile), 256 threads per row tile: running maximum (moved
 //                only when it grows by more than 8 in log2 units), P as 16-bit
 //                pairs in TMEM, fp32 sums, O rescaled in TMEM when the maximum
 //                moved, and O / l at the end.
+// Both row tiles take every key tile of the item, so they alternate strictly;
+// the products of key tiles that a row tile does not see at all (one in
+// several) have weight 0.
 // TMEM, D = 128: one S buffer that the row tiles take in turn [0, 128), P
 // [128, 192) and [192, 256), O [256, 384) and [384, 512); a tile's logits leave
 // S for registers at once, so the buffer is free again while its softmax runs.
@@ -49,7 +55,7 @@ constexpr int BK = 128;        // keys per tile
 constexpr int kRows = 128;     // rows per row tile
 constexpr int HK = BK / 2;     // keys per softmax thread
 constexpr int kSoftWarps = 16;
-constexpr int kThreads = 32 * (2 + kSoftWarps);
+constexpr int kThreads = 32 * (4 + kSoftWarps);
 constexpr int kStages = 2;
 constexpr int kMaxSeqs = 256;  // sequences per launch (their table is a kernel argument)
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
@@ -100,14 +106,26 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+// True in one lane of the (converged) warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// A work item: sequence, key head, the row tiles' first tokens and key tiles.
+// The k-th item of this CTA, or n_items and more: CTAs take items in turn,
+// forwards and backwards, so that with items sorted by size every CTA's share is alike.
+__device__ __forceinline__ int nth_item(int k) {
+  return k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+// A work item: sequence, key head, the first token of its row tiles, its key tiles.
 struct Item {
   int q0, k0, q_len, kv_len, head, tok0;
-  int n[2];    // key tiles of each row tile
+  int n;       // key tiles
   int shift;   // kv_len - q_len
   __device__ __forceinline__ int tok(int t, int tpt) const { return tok0 + t * tpt; }
 };
@@ -126,11 +144,8 @@ __device__ __forceinline__ Item item_of(const Args& a, int idx) {
   it.head = r % a.kv_heads;
   it.tok0 = (tiles - 1 - r / a.kv_heads) * 2 * a.tpt;
   it.shift = it.kv_len - it.q_len;
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int first = it.tok(t, a.tpt), last = min(it.q_len, first + a.tpt) - 1;
-    it.n[t] = first < it.q_len ? max(0, (it.shift + last + 1 + BK - 1) / BK) : 0;
-  }
+  const int end = it.shift + min(it.q_len, it.tok0 + 2 * a.tpt);  // keys that the last row sees
+  it.n = max(0, (end + BK - 1) / BK);
   return it;
 }
 
@@ -163,15 +178,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   uint32_t* flags = reinterpret_cast<uint32_t*>(smem + C::kFlags);  // [2][16]
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the warp index as a warp-uniform value, so that its branches and what they compute stay uniform
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(q_full), 1);
-    mbar_init(smem_u32(q_empty), 1);
+    mbar_init(smem_u32(q_empty), 2);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(k_full + s), 1);
-      mbar_init(smem_u32(k_empty + s), 1);
+      mbar_init(smem_u32(k_empty + s), 2);
       mbar_init(smem_u32(v_full + s), 1);
-      mbar_init(smem_u32(v_empty + s), 1);
+      mbar_init(smem_u32(v_empty + s), 2);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(s_full + t), 1);
@@ -205,14 +221,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_bytes = 128u * args.group * args.tpt * (D / 64);
       uint32_t kc = 0, vc = 0, qc = 0;
       bool ok = true;
-      for (int idx = blockIdx.x; ok && idx < n_items; idx += gridDim.x) {
+      for (int w = 0, idx; ok && (idx = nth_item(w)) < n_items; ++w) {
         const Item it = item_of(args, idx);
-        const int n = max(it.n[0], it.n[1]);
+        const int n = it.n, tiles = it.tok(1, args.tpt) < it.q_len ? 2 : 1;
         if (n == 0) continue;
         if (!mbar_wait(smem_u32(q_empty), (qc & 1) ^ 1, abort_v, args.status)) break;
         const uint32_t qb = smem_u32(q_full);
-        mbar_arrive_expect_tx(qb, q_bytes * (it.n[1] > 0 ? 2 : 1));
-        for (int t = 0; t < (it.n[1] > 0 ? 2 : 1); ++t)
+        mbar_arrive_expect_tx(qb, q_bytes * tiles);
+        for (int t = 0; t < tiles; ++t)
           for (int x = 0; x < D / 64; ++x)
             tma_load_3d(smem_u32(smem + C::kQ + t * C::kTile + x * C::kSub), &tm_q, qb, 64 * x, it.head * args.group,
                         it.q0 + it.tok(t, args.tpt));
@@ -241,69 +257,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc16<T>(kRows, BK);
-      constexpr uint32_t idesc_o = idesc16<T>(kRows, D, /*b_mn_major=*/true);
-      uint32_t kc = 0, vc = 0, qc = 0;
-      uint32_t sc[2] = {0, 0}, pc[2] = {0, 0};  // S tiles per buffer and P tiles per row tile so far
-      bool ok = true;
-      for (int idx = blockIdx.x; ok && idx < n_items; idx += gridDim.x) {
-        const Item it = item_of(args, idx);
-        const int n = max(it.n[0], it.n[1]);
-        if (n == 0) continue;
-        if (!mbar_wait(smem_u32(q_full), qc & 1, abort_v, args.status)) break;
-        for (int j = 0; ok && j <= n; ++j) {
-          const uint32_t ks = kc % kStages, vs = vc % kStages;
-          if (j < n && !(ok = mbar_wait(smem_u32(k_full + ks), (kc / kStages) & 1, abort_v, args.status))) break;
-          bool v_ready = false;
+  } else if (warp < 3) {
+    // The whole warp walks the loop and one elected lane issues: descriptors
+    // and addresses then live in uniform registers.
+    const int t = warp - 1;
+    constexpr uint32_t idesc_s = idesc16<T>(kRows, BK);
+    constexpr uint32_t idesc_o = idesc16<T>(kRows, D, /*b_mn_major=*/true);
+    const uint64_t qdesc = smem_desc_sw128(smem_u32(smem + C::kQ + t * C::kTile));
+    const uint64_t kdesc = smem_desc_sw128(smem_u32(smem + C::kK));
+    const uint64_t vdesc = smem_desc_sw128(smem_u32(smem + C::kV), 1024, C::kSub);
+    const uint32_t s_at = tmem + C::s_col(t), p_at = tmem + C::p_col(t), o_at = tmem + C::o_col(t);
+    const uint32_t bar0 = smem_u32(bars);
+    auto bar = [&](const uint64_t* x) { return bar0 + static_cast<uint32_t>(x - bars) * 8; };
+    auto wait = [&](const uint64_t* x, uint32_t parity) {
+      return mbar_wait_warp(bar(x), parity, abort_v, args.status);
+    };
+    // the S buffer is free once the softmax has copied what was last put into it:
+    // this tile's logits (D = 64), or the other tile's, S_0 S_1 S_0 ... (D = 128)
+    const uint64_t* s_prev = s_free + (D == 128 ? 1 - t : t);
+    const uint32_t s_lag = D == 128 && t == 1 ? 0 : 1;
+    uint32_t kc = 0, vc = 0, qc = 0;  // K, V and Q tiles so far (S and P run with K and V)
+    bool ok = true;
+    for (int w = 0, idx; ok && (idx = nth_item(w)) < n_items; ++w) {
+      const Item it = item_of(args, idx);
+      const int n = it.n;
+      if (n == 0) continue;
+      if (!(ok = wait(q_full, qc & 1))) break;
+      for (int j = 0; j <= n; ++j) {
+        if (j < n) {
+          const uint32_t ks = kc % kStages;
+          if (!(ok = wait(k_full + ks, (kc / kStages) & 1))) break;
+          if (kc >= s_lag && !(ok = wait(s_prev, (kc - s_lag) & 1))) break;
+          tc_fence_after();
+          const uint64_t kd = kdesc + ks * (C::kTile / 16);
+          if (elect_one()) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (j < it.n[t]) {
-              // the buffer's last logits have left for registers
-              const int b = D == 128 ? 0 : t;
-              if (sc[b] > 0 && !(ok = mbar_wait(smem_u32(s_free + b), (sc[b] - 1) & 1, abort_v, args.status))) break;
-              tc_fence_after();
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (k / 4) * C::kSub;
-                umma_bf16_ss(tmem + C::s_col(t), smem_desc_sw128(smem_u32(smem + C::kQ + t * C::kTile + off)) + 2 * (k % 4),
-                             smem_desc_sw128(smem_u32(smem + C::kK + ks * C::kTile + off)) + 2 * (k % 4), idesc_s,
-                             k > 0 ? 1u : 0u);
-              }
-              umma_commit(smem_u32(s_full + t));
-              ++sc[b];
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k / 4) * (C::kSub / 16) + 2 * (k % 4);
+              umma_bf16_ss(s_at, qdesc + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
             }
-            // the last user of this K tile: row tile 1, or 0 where 1 has fewer tiles
-            if (j < n && t == 1) umma_commit(smem_u32(k_empty + ks));
-            if (j == n - 1 && t == 1) umma_commit(smem_u32(q_empty));
-            if (j > 0 && j <= it.n[t]) {
-              // P is written by the threads that read O at the end of an item, after they did
-              if (!(ok = mbar_wait(smem_u32(p_full + t), pc[t] & 1, abort_v, args.status))) break;
-              if (!v_ready && !(ok = mbar_wait(smem_u32(v_full + vs), (vc / kStages) & 1, abort_v, args.status))) break;
-              v_ready = true;
-              tc_fence_after();
-              const uint64_t vdesc = smem_desc_sw128(smem_u32(smem + C::kV + vs * C::kTile), 1024, C::kSub);
-#pragma unroll
-              for (int kk = 0; kk < BK / 16; ++kk)  // 16 keys: 8 TMEM columns of pairs, 2048 bytes of V
-                umma_bf16_ts(tmem + C::o_col(t), tmem + C::p_col(t) + 8 * kk, vdesc + 128 * kk, idesc_o,
-                             (j > 1 || kk > 0) ? 1u : 0u);
-              umma_commit(smem_u32(o_done + t));
-              ++pc[t];
-            }
-            if (j > 0 && t == 1) umma_commit(smem_u32(v_empty + vs));
+            umma_commit(bar(s_full + t));
+            umma_commit(bar(k_empty + ks));
+            if (j == n - 1) umma_commit(bar(q_empty));
           }
-          if (j < n) ++kc;
-          if (j > 0) ++vc;
+          __syncwarp();
+          ++kc;
         }
-        ++qc;
+        if (j > 0) {
+          const uint32_t vs = vc % kStages;
+          if (!(ok = wait(v_full + vs, (vc / kStages) & 1))) break;
+          // P is written by the threads that read O at the end of an item, after they did
+          if (!(ok = wait(p_full + t, vc & 1))) break;
+          tc_fence_after();
+          const uint64_t vd = vdesc + vs * (C::kTile / 16);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk)  // 16 keys: 8 TMEM columns of pairs, 2048 bytes of V
+              umma_bf16_ts(o_at, p_at + 8 * kk, vd + 128 * kk, idesc_o, (j > 1 || kk > 0) ? 1u : 0u);
+            umma_commit(bar(o_done + t));
+            umma_commit(bar(v_empty + vs));
+          }
+          __syncwarp();
+          ++vc;
+        }
       }
+      ++qc;
     }
-  } else {
-    const int t = (warp - 2) >> 3, hf = ((warp - 2) >> 2) & 1, quad = warp & 3;
+  } else if (warp >= 4) {
+    const int t = (warp - 4) >> 3, hf = ((warp - 4) >> 2) & 1, quad = warp & 3;
     const int r = quad * 32 + lane;            // row of the tile = TMEM lane
     const int pair_id = 1 + t * 4 + quad;      // named barrier of the two warps of these rows
-    const int tid = (warp - 2 - 8 * t) * 32 + lane;  // 0..255 in the row tile's threads
+    const int tid = (warp - 4 - 8 * t) * 32 + lane;  // 0..255 in the row tile's threads
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     float* xmax = reinterpret_cast<float*>(smem + C::kXch) + t * 4 * kRows;
     float* xsum = reinterpret_cast<float*>(smem + C::kXch) + 8 * kRows + t * 2 * kRows;
@@ -313,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // A warp whose wait failed keeps meeting the others at the named barriers,
     // doing nothing else, so that none of them waits for it.
-    for (int idx = blockIdx.x; idx < n_items; idx += gridDim.x, ++items) {
+    for (int idx; (idx = nth_item(items)) < n_items; ++items) {
       const Item it = item_of(args, idx);
       const int tok = it.tok(t, args.tpt) + row_tok;
       const bool live = tok < it.q_len && row_tok < args.tpt;
@@ -324,7 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // everyone has left the item before last, whose notes shared this set's twin
       bar_sync(9, kSoftWarps * 32);
       if (t == 0 && tid < 16) flags[16 * ((items & 1) ^ 1) + tid] = 0;
-      const int n = it.n[t], n_max = max(it.n[0], it.n[1]);
+      const int n = it.n;
+      const bool idle = it.tok(t, args.tpt) >= it.q_len;  // a row tile without tokens
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
         if (ok) ok = mbar_wait_warp(smem_u32(s_full + t), sc & 1, abort_v, args.status);
@@ -334,10 +359,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         tc_fence_after();
+        if (idle) {
+          bar_sync(pair_id, 64);
+          mbar_arrive(smem_u32(s_free + t));
+          if (j > 0) ok = mbar_wait_warp(smem_u32(o_done + t), (oc - 1) & 1, abort_v, args.status);
+          if (ok) mbar_arrive(smem_u32(p_full + t));
+          ++oc;
+          continue;
+        }
         uint32_t u[HK];
         tmem_ld64(trow + C::s_col(t) + HK * hf, u);
         tc_fence_before();
-        mbar_arrive(smem_u32(s_free + (D == 128 ? 0 : t)));
+        mbar_arrive(smem_u32(s_free + t));
         const bool masked = (j + 1) * BK > lim_min;
         if (masked) {
           const int nvalid = lim - j * BK - HK * hf;
@@ -377,8 +410,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st32(col, o);
           }
         }
-        if (masked && (t == 0 || j >= it.n[0])) {
-          // look this V tile over before its first product
+        if (masked) {
+          // Look this V tile over before its product. Both row tiles' threads do so; what
+          // one writes the other would write as well.
           const uint32_t vc = vc_item + j, vs = vc % kStages;
           ok = mbar_wait_warp(smem_u32(v_full + vs), (vc / kStages) & 1, abort_v, args.status);
           if (ok) {
@@ -398,9 +432,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               w.y &= ~__vcmpeq2(w.y & e, e);
               w.z &= ~__vcmpeq2(w.z & e, e);
               w.w &= ~__vcmpeq2(w.w & e, e);
-              *at = w;
               const int key = j * BK + row - flag_base;
               if (key >= 0 && key < 512) atomicOr(flag + (key >> 5), 1u << (key & 31));
+              __threadfence_block();  // whoever finds the value replaced finds the note
+              *at = w;
             }
             fence_proxy_async_smem();
           }
@@ -460,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
-      vc_item += n_max;
+      vc_item += n;
     }
   }
 
