@@ -125,3 +125,22 @@ def test_sequences_are_independent_and_results_repeat():
         alone = vlm.prompt_attention(q[at:at + m], k[at:at + m], v[at:at + m], [m])
         assert torch.equal(both[at:at + m], alone)
         at += m
+
+
+def test_more_work_items_than_one_launch_takes():
+    # 128 heads on one key head: 2 tokens per item; only the last 64 queries see a key
+    q_len, kv_len, heads, dim = 160_000, 64, 128, 64
+    k, v = U.rand16(1, (kv_len, 1, dim), torch.bfloat16), U.rand16(2, (kv_len, 1, dim), torch.bfloat16)
+    q = torch.randn((q_len, heads, dim), generator=torch.Generator("cuda").manual_seed(3), device="cuda",
+                    dtype=torch.bfloat16)
+    out = torch.full_like(q, 7.0)
+    status = vlm.new_status()
+    before = vlm.launch_count()
+    vlm.prompt_attention(q, k.cuda(), v.cuda(), [q_len], [kv_len], out=out, status=status)
+    assert vlm.launch_count() - before > 1
+    assert vlm.status_sync(status) == vlm.OK
+    assert not out[:q_len - kv_len].any()
+    ql = q[q_len - kv_len:].float().cpu().numpy()
+    o, a = T.prompt_attention(ql, k.float().numpy(), v.float().numpy(), [kv_len], [kv_len], dim ** -0.5)
+    ds = U.logit_error(ql, k.float().numpy(), dim ** -0.5)
+    U.assert_close(out[q_len - kv_len:], o, U.prompt_tolerance(torch.bfloat16, o, a, ds))

@@ -58,12 +58,16 @@ constexpr int kSoftWarps = 16;
 constexpr int kThreads = 32 * (4 + kSoftWarps);
 constexpr int kStages = 2;
 constexpr int kMaxSeqs = 256;  // sequences per launch (their table is a kernel argument)
+constexpr int kItemSlots = 512;  // items per CTA and launch
+constexpr int kIssueRegs = 32, kSoftRegs = 112;
+static_assert(128 * kIssueRegs + 32 * kSoftWarps * kSoftRegs <= kThreads * 96, "the launch's registers");
+constexpr int kSets = 8;       // items whose noted keys are kept apart
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
 struct SeqTable {
   int n;
   int off[kMaxSeqs + 1];  // work items before each sequence
-  int q0[kMaxSeqs], k0[kMaxSeqs], q_len[kMaxSeqs], kv_len[kMaxSeqs];
+  int q0[kMaxSeqs], k0[kMaxSeqs], q_len[kMaxSeqs], kv_len[kMaxSeqs], tiles[kMaxSeqs];  // tiles: items per key head
 };
 
 struct Args {
@@ -84,8 +88,9 @@ struct Cfg {
   static constexpr int kQ = 0, kK = 2 * kTile, kV = kK + kStages * kTile;
   static constexpr int kBars = kV + kStages * kTile;
   static constexpr int kXch = kBars + 256;         // row maxima [tile][parity][half][row], sums [tile][half][row]
-  static constexpr int kFlags = kXch + (8 + 4) * kRows * 4;  // noted keys, two sets of 512 bits
-  static constexpr int kSmem = kFlags + 2 * 64 + 1024;
+  static constexpr int kFlags = kXch + (8 + 4) * kRows * 4;  // noted keys, kSets sets of 512 bits
+  static constexpr int kItems = kFlags + kSets * 64;         // this CTA's first items, decoded
+  static constexpr int kSmem = kItems + kItemSlots * 32 + 1024;
   static constexpr uint32_t s_col(int t) { return D == 128 ? 0 : 128 * t; }
   static constexpr uint32_t p_col(int t) { return D == 128 ? 128 + 64 * t : 256 + 64 * t; }
   static constexpr uint32_t o_col(int t) { return D == 128 ? 256 + 128 * t : 384 + 64 * t; }
@@ -107,23 +112,102 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 // True in one lane of the (converged) warp, the same one each time.
-__device__ __forceinline__ bool elect_one() {
+__device__ __forceinline__ uint32_t elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
+  return p;
+}
+// tcgen05 instructions issued by the lane with `go` set, as predicated
+// instructions of the whole warp: in a divergent branch their operands would
+// have to be moved into uniform registers one by one.
+__device__ __forceinline__ void mma_ss(uint32_t go, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(go)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t go, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(go)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t go, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(go)
+      : "memory");
+}
+// One arrival for a warp, after all its lanes got here: arrivals of single
+// threads on one barrier are taken one after the other.
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+// a + 0 b on 16-bit pairs: 0 as long as every b is finite, NaN from then on.
+template <typename T>
+__device__ __forceinline__ uint32_t add_zero_times(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (is_half<T>)
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(b), "r"(0u), "r"(a));
+  else
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(b), "r"(0u), "r"(a));
+  return d;
+}
+// mbar_wait_warp that polls instead of suspending the warp: for the two issuing
+// warps, whose wake-up the whole key tile waits for.
+__device__ __forceinline__ bool mbar_poll_warp(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  auto test = [&]() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  if (__all_sync(0xffffffffu, test())) return true;
+  const long long t0 = clock64();
+  for (uint32_t i = 1;; ++i) {
+    if (__all_sync(0xffffffffu, test())) return true;
+    if ((i & 255u) == 0) {
+      bool stop = *abort != 0;
+      if (!stop && clock64() - t0 > kWaitBudgetCycles) {
+        *abort = 1;
+        set_status(status, VLM_ERR_TIMEOUT);
+        stop = true;
+      }
+      if (__any_sync(0xffffffffu, stop)) return false;
+    }
+  }
+}
+// 32 bytes in one instruction where they are aligned to it: a warp's rows lie
+// apart, so each store instruction costs one pass per lane.
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// The k-th item of this CTA, or n_items and more: CTAs take items in turn,
+// The k-th item of this CTA in the launch's list, or n_items and more: CTAs take items in turn,
 // forwards and backwards, so that with items sorted by size every CTA's share is alike.
 __device__ __forceinline__ int nth_item(int k) {
   return k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
 // A work item: sequence, key head, the first token of its row tiles, its key tiles.
-struct Item {
+struct alignas(16) Item {
   int q0, k0, q_len, kv_len, head, tok0;
   int n;       // key tiles
   int shift;   // kv_len - q_len
@@ -140,25 +224,20 @@ __device__ __forceinline__ Item item_of(const Args& a, int idx) {
   it.k0 = a.t.k0[lo];
   it.q_len = a.t.q_len[lo];
   it.kv_len = a.t.kv_len[lo];
-  const int r = idx - a.t.off[lo], tiles = (a.t.off[lo + 1] - a.t.off[lo]) / a.kv_heads;
-  it.head = r % a.kv_heads;
-  it.tok0 = (tiles - 1 - r / a.kv_heads) * 2 * a.tpt;
+  const int r = idx - a.t.off[lo], row = r / a.kv_heads;
+  it.head = r - row * a.kv_heads;
+  it.tok0 = (a.t.tiles[lo] - 1 - row) * 2 * a.tpt;
   it.shift = it.kv_len - it.q_len;
   const int end = it.shift + min(it.q_len, it.tok0 + 2 * a.tpt);  // keys that the last row sees
   it.n = max(0, (end + BK - 1) / BK);
   return it;
 }
 
-template <typename T>
-__device__ __forceinline__ bool finite16(uint32_t w) {
-  constexpr uint32_t m = is_half<T> ? 0x7C007C00u : 0x7F807F80u;
-  return __vcmpeq2(w & m, m) == 0;
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Args args, int n_items) {
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Args args, int first_item,
+                       int n_items) {
   using C = Cfg<D>;
   constexpr bool kHalf = is_half<T>;
   extern __shared__ uint8_t smem_raw[];
@@ -176,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* o_done = p_full + 2;         // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 2);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  uint32_t* flags = reinterpret_cast<uint32_t*>(smem + C::kFlags);  // [2][16]
+  uint32_t* flags = reinterpret_cast<uint32_t*>(smem + C::kFlags);  // [kSets][16]
 
   // the warp index as a warp-uniform value, so that its branches and what they compute stay uniform
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -191,14 +270,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(s_full + t), 1);
-      mbar_init(smem_u32(s_free + t), 256);
-      mbar_init(smem_u32(p_full + t), 256);
+      mbar_init(smem_u32(s_free + t), kSoftWarps / 2);
+      mbar_init(smem_u32(p_full + t), kSoftWarps / 2);
       mbar_init(smem_u32(o_done + t), 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (threadIdx.x < 32) flags[threadIdx.x] = 0;
+  if (threadIdx.x < kSets * 16) flags[threadIdx.x] = 0;
+  // Decoding an item (divisions, indexed argument loads) takes some 2,000 cycles in
+  // the middle of the pipeline, so it is done for the whole list at the start.
+  Item* items_s = reinterpret_cast<Item*>(smem + C::kItems);
+  for (int k = threadIdx.x; k < kItemSlots; k += kThreads) {
+    const int idx = nth_item(k);
+    if (idx >= n_items) break;
+    items_s[k] = item_of(args, first_item + idx);
+  }
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
@@ -215,14 +302,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_v = abort_flag;
   griddep_wait();
   griddep_launch_dependents();
+  // 640 threads x 96 registers at launch: the issuing warps give some up to the softmax
+  if (warp < 4)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+  else
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
 
   if (warp == 0) {
     if (lane == 0) {
       const uint32_t q_bytes = 128u * args.group * args.tpt * (D / 64);
       uint32_t kc = 0, vc = 0, qc = 0;
       bool ok = true;
-      for (int w = 0, idx; ok && (idx = nth_item(w)) < n_items; ++w) {
-        const Item it = item_of(args, idx);
+      for (int w = 0; ok && nth_item(w) < n_items; ++w) {
+        const Item it = items_s[w];
         const int n = it.n, tiles = it.tok(1, args.tpt) < it.q_len ? 2 : 1;
         if (n == 0) continue;
         if (!mbar_wait(smem_u32(q_empty), (qc & 1) ^ 1, abort_v, args.status)) break;
@@ -261,6 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The whole warp walks the loop and one elected lane issues: descriptors
     // and addresses then live in uniform registers.
     const int t = warp - 1;
+    const uint32_t go = elect_one();
     constexpr uint32_t idesc_s = idesc16<T>(kRows, BK);
     constexpr uint32_t idesc_o = idesc16<T>(kRows, D, /*b_mn_major=*/true);
     const uint64_t qdesc = smem_desc_sw128(smem_u32(smem + C::kQ + t * C::kTile));
@@ -270,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t bar0 = smem_u32(bars);
     auto bar = [&](const uint64_t* x) { return bar0 + static_cast<uint32_t>(x - bars) * 8; };
     auto wait = [&](const uint64_t* x, uint32_t parity) {
-      return mbar_wait_warp(bar(x), parity, abort_v, args.status);
+      return mbar_poll_warp(bar(x), parity, abort_v, args.status);
     };
     // the S buffer is free once the softmax has copied what was last put into it:
     // this tile's logits (D = 64), or the other tile's, S_0 S_1 S_0 ... (D = 128)
@@ -278,8 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_lag = D == 128 && t == 1 ? 0 : 1;
     uint32_t kc = 0, vc = 0, qc = 0;  // K, V and Q tiles so far (S and P run with K and V)
     bool ok = true;
-    for (int w = 0, idx; ok && (idx = nth_item(w)) < n_items; ++w) {
-      const Item it = item_of(args, idx);
+    for (int w = 0; ok && nth_item(w) < n_items; ++w) {
+      const Item it = items_s[w];
       const int n = it.n;
       if (n == 0) continue;
       if (!(ok = wait(q_full, qc & 1))) break;
@@ -290,17 +383,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kc >= s_lag && !(ok = wait(s_prev, (kc - s_lag) & 1))) break;
           tc_fence_after();
           const uint64_t kd = kdesc + ks * (C::kTile / 16);
-          if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = (k / 4) * (C::kSub / 16) + 2 * (k % 4);
-              umma_bf16_ss(s_at, qdesc + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
-            }
-            umma_commit(bar(s_full + t));
-            umma_commit(bar(k_empty + ks));
-            if (j == n - 1) umma_commit(bar(q_empty));
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * (C::kSub / 16) + 2 * (k % 4);
+            mma_ss(go, s_at, qdesc + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
           }
-          __syncwarp();
+          mma_commit(go, bar(s_full + t));
+          mma_commit(go, bar(k_empty + ks));
+          if (j == n - 1) mma_commit(go, bar(q_empty));
           ++kc;
         }
         if (j > 0) {
@@ -310,14 +400,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait(p_full + t, vc & 1))) break;
           tc_fence_after();
           const uint64_t vd = vdesc + vs * (C::kTile / 16);
-          if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk)  // 16 keys: 8 TMEM columns of pairs, 2048 bytes of V
-              umma_bf16_ts(o_at, p_at + 8 * kk, vd + 128 * kk, idesc_o, (j > 1 || kk > 0) ? 1u : 0u);
-            umma_commit(bar(o_done + t));
-            umma_commit(bar(v_empty + vs));
-          }
-          __syncwarp();
+          for (int kk = 0; kk < BK / 16; ++kk)  // 16 keys: 8 TMEM columns of pairs, 2048 bytes of V
+            mma_ts(go, o_at, p_at + 8 * kk, vd + 128 * kk, idesc_o, (j > 1 || kk > 0) ? 1u : 0u);
+          mma_commit(go, bar(o_done + t));
+          mma_commit(go, bar(v_empty + vs));
           ++vc;
         }
       }
@@ -333,26 +420,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* xsum = reinterpret_cast<float*>(smem + C::kXch) + 8 * kRows + t * 2 * kRows;
     const uint64_t sl2x2 = pair_f32(args.sl2);
     const int row_tok = r / args.group, row_head = r - row_tok * args.group;
-    uint32_t sc = 0, oc = 0, vc_item = 0, items = 0;
+    const bool wide = ((reinterpret_cast<uintptr_t>(args.out) | (args.out_stride * 2)) & 31) == 0;
+    uint32_t sc = 0, oc = 0, vc_item = 0, live_items = 0;
+    int items = 0;
     bool ok = true;
-    // A warp whose wait failed keeps meeting the others at the named barriers,
-    // doing nothing else, so that none of them waits for it.
-    for (int idx; (idx = nth_item(items)) < n_items; ++items) {
-      const Item it = item_of(args, idx);
+    // A warp whose wait failed keeps meeting its partner at the named barrier,
+    // doing nothing else, so that the partner never waits for it.
+    for (; nth_item(items) < n_items; ++items) {
+      const Item it = items_s[items];
       const int tok = it.tok(t, args.tpt) + row_tok;
       const bool live = tok < it.q_len && row_tok < args.tpt;
       const int lim = it.shift + tok + 1;                     // the row sees keys [0, lim)
       const int lim_min = it.shift + it.tok(t, args.tpt) + 1;  // what every row of the tile sees
       const int flag_base = max(0, it.shift + it.tok0 + 1) / BK * BK;
-      uint32_t* flag = flags + 16 * (items & 1);
-      // everyone has left the item before last, whose notes shared this set's twin
-      bar_sync(9, kSoftWarps * 32);
-      if (t == 0 && tid < 16) flags[16 * ((items & 1) ^ 1) + tid] = 0;
+      // The row tiles' threads are at most three key tiles apart (two K stages and the
+      // alternation of S), so the notes of four items back are no longer in use: cleared
+      // here for the item four ahead. Items without keys have no notes and do not count.
+      uint32_t* flag = flags + 16 * (live_items % kSets);
+      if (it.n > 0) {
+        if (t == 0 && tid < 16) flags[16 * ((live_items + kSets / 2) % kSets) + tid] = 0;
+        ++live_items;
+      }
       const int n = it.n;
       const bool idle = it.tok(t, args.tpt) >= it.q_len;  // a row tile without tokens
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
-        if (ok) ok = mbar_wait_warp(smem_u32(s_full + t), sc & 1, abort_v, args.status);
+        if (ok) ok = mbar_poll_warp(smem_u32(s_full + t), sc & 1, abort_v, args.status);
         ++sc;
         if (!ok) {
           bar_sync(pair_id, 64);
@@ -361,16 +454,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (idle) {
           bar_sync(pair_id, 64);
-          mbar_arrive(smem_u32(s_free + t));
+          warp_arrive(smem_u32(s_free + t), lane);
           if (j > 0) ok = mbar_wait_warp(smem_u32(o_done + t), (oc - 1) & 1, abort_v, args.status);
-          if (ok) mbar_arrive(smem_u32(p_full + t));
+          if (ok) warp_arrive(smem_u32(p_full + t), lane);
           ++oc;
           continue;
         }
         uint32_t u[HK];
         tmem_ld64(trow + C::s_col(t) + HK * hf, u);
         tc_fence_before();
-        mbar_arrive(smem_u32(s_free + t));
+        warp_arrive(smem_u32(s_free + t), lane);
         const bool masked = (j + 1) * BK > lim_min;
         if (masked) {
           const int nvalid = lim - j * BK - HK * hf;
@@ -417,32 +510,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait_warp(smem_u32(v_full + vs), (vc / kStages) & 1, abort_v, args.status);
           if (ok) {
             const int valid = it.kv_len - j * BK;
-            for (int x = tid; x < BK * D / 8; x += 256) {
-              const int sub = x / (BK * 8), row = (x >> 3) % BK, ch = x & 7;
-              uint4* at = reinterpret_cast<uint4*>(smem + C::kV + vs * C::kTile + sub * C::kSub + row * 128 +
-                                                   ((ch ^ (row & 7)) << 4));
-              if (row >= valid) {
-                *at = make_uint4(0, 0, 0, 0);
-                continue;
+            constexpr int kChunks = BK * D / 8 / 256;  // 16-byte chunks per thread
+            constexpr uint32_t e = kHalf ? 0x7C007C00u : 0x7F807F80u;
+            uint8_t* tile = smem + C::kV + vs * C::kTile;
+            // chunk x of the thread: row tid / 8 + 32 (x % 4), column group tid % 8 of 64-column box x / 4
+            uint8_t* mine = tile + (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) << 4);
+            uint32_t odd = 0;
+#pragma unroll
+            for (int x = 0; x < kChunks; ++x) {
+              const uint4 w = *reinterpret_cast<const uint4*>(mine + (x / 4) * C::kSub + (x % 4) * 4096);
+              odd = add_zero_times<T>(add_zero_times<T>(odd, w.x), w.y);
+              odd = add_zero_times<T>(add_zero_times<T>(odd, w.z), w.w);
+            }
+            if ((odd & 0x7FFF7FFFu) != 0 || valid < BK) {
+#pragma unroll 1
+              for (int x = 0; x < kChunks; ++x) {
+                const int row = (tid >> 3) + 32 * (x % 4);
+                uint4* at = reinterpret_cast<uint4*>(mine + (x / 4) * C::kSub + (x % 4) * 4096);
+                if (row >= valid) {
+                  *at = make_uint4(0, 0, 0, 0);
+                } else {
+                  uint4 w = *at;
+                  if ((__vcmpeq2(w.x & e, e) | __vcmpeq2(w.y & e, e) | __vcmpeq2(w.z & e, e) | __vcmpeq2(w.w & e, e)) == 0)
+                    continue;
+                  w.x &= ~__vcmpeq2(w.x & e, e);
+                  w.y &= ~__vcmpeq2(w.y & e, e);
+                  w.z &= ~__vcmpeq2(w.z & e, e);
+                  w.w &= ~__vcmpeq2(w.w & e, e);
+                  const int key = j * BK + row - flag_base;
+                  if (key >= 0 && key < 512) atomicOr(flag + (key >> 5), 1u << (key & 31));
+                  __threadfence_block();  // whoever finds the value replaced finds the note
+                  *at = w;
+                }
               }
-              uint4 w = *at;
-              if (finite16<T>(w.x) && finite16<T>(w.y) && finite16<T>(w.z) && finite16<T>(w.w)) continue;
-              constexpr uint32_t e = kHalf ? 0x7C007C00u : 0x7F807F80u;
-              w.x &= ~__vcmpeq2(w.x & e, e);
-              w.y &= ~__vcmpeq2(w.y & e, e);
-              w.z &= ~__vcmpeq2(w.z & e, e);
-              w.w &= ~__vcmpeq2(w.w & e, e);
-              const int key = j * BK + row - flag_base;
-              if (key >= 0 && key < 512) atomicOr(flag + (key >> 5), 1u << (key & 31));
-              __threadfence_block();  // whoever finds the value replaced finds the note
-              *at = w;
             }
             fence_proxy_async_smem();
           }
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(smem_u32(p_full + t));
+        warp_arrive(smem_u32(p_full + t), lane);
         ++oc;
       }
       xsum[hf * kRows + r] = l;
@@ -453,8 +560,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         uint32_t noted = 0;
-        if (n > 0)
-          for (int i = 0; i < 16; ++i) noted |= *reinterpret_cast<volatile uint32_t*>(flag + i);
+        if (n > 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 w = reinterpret_cast<const uint4*>(flag)[i];
+            noted |= w.x | w.y | w.z | w.w;
+          }
+        }
         T* dst = static_cast<T*>(args.out) + static_cast<int64_t>(it.q0 + tok) * args.out_stride +
                  (it.head * args.group + row_head) * D + (D / 2) * hf;
 #pragma unroll
@@ -482,14 +594,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
-            uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * x);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t w[4];
+            for (int i = 0; i < 2; ++i) {
+              uint32_t w[8];
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = pack16<T>(__uint_as_float(o[8 * i + 2 * k]), __uint_as_float(o[8 * i + 2 * k + 1]));
-              d4[i] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int k = 0; k < 8; ++k)
+                w[k] = pack16<T>(__uint_as_float(o[16 * i + 2 * k]), __uint_as_float(o[16 * i + 2 * k + 1]));
+              store32(dst + 32 * x + 16 * i, w, wide);
             }
           }
         }
@@ -580,7 +691,8 @@ int launch_prompt_attention(const PromptAttn& p, cudaStream_t s) {
         a.t.k0[k] = k0[x];
         a.t.q_len[k] = p.q_lens[x];
         a.t.kv_len[k] = p.kv_lens[x];
-        items += (static_cast<int64_t>(p.q_lens[x]) + 2 * tpt - 1) / (2 * tpt) * p.kv_heads;
+        a.t.tiles[k] = static_cast<int>((static_cast<int64_t>(p.q_lens[x]) + 2 * tpt - 1) / (2 * tpt));
+        items += static_cast<int64_t>(a.t.tiles[k]) * p.kv_heads;
         if (items > 0x7FFFFFFF - 65536) return VLM_ERR_BAD_SHAPE;
       }
       if (a.t.n == 0) continue;
@@ -594,11 +706,14 @@ int launch_prompt_attention(const PromptAttn& p, cudaStream_t s) {
       a.out = p.out;
       a.out_stride = p.out_stride;
       a.status = p.status;
-      const int grid = static_cast<int>(std::min<int64_t>(items, num_sms()));
-      const cudaError_t e =
-          launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, tq, tk, tv, a, static_cast<int>(items));
-      if (e != cudaSuccess) return VLM_ERR_CUDA;
-      ++launches;
+      for (int64_t at = 0; at < items;) {
+        const int n = static_cast<int>(std::min<int64_t>(items - at, static_cast<int64_t>(num_sms()) * kItemSlots));
+        const cudaError_t e = launch_pdl(kern, dim3(std::min(n, num_sms())), dim3(kThreads), smem, s, tq, tk, tv, a,
+                                         static_cast<int>(at), n);
+        if (e != cudaSuccess) return VLM_ERR_CUDA;
+        at += n;
+        ++launches;
+      }
     }
     note_extra_launches(launches - 1);
     return VLM_OK;
