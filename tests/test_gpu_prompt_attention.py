@@ -144,3 +144,14 @@ def test_more_work_items_than_one_launch_takes():
     o, a = T.prompt_attention(ql, k.float().numpy(), v.float().numpy(), [kv_len], [kv_len], dim ** -0.5)
     ds = U.logit_error(ql, k.float().numpy(), dim ** -0.5)
     U.assert_close(out[q_len - kv_len:], o, U.prompt_tolerance(torch.bfloat16, o, a, ds))
+
+
+@pytest.mark.parametrize("dtype,gain", [(torch.bfloat16, 1e7), (torch.float16, 1e4)])
+def test_logits_of_any_size(dtype, gain):
+    # the largest logit of a row, up to 10^15, has all the weight
+    heads, dim, n = 4, 128, 200
+    q, k = U.rand16(1, (n, heads, dim), dtype, gain), U.rand16(2, (n, 2, dim), dtype, gain)
+    v = U.rand16(3, (n, 2, dim), dtype)
+    o, _ = T.prompt_attention(q.float().numpy(), k.float().numpy(), v.float().numpy(), [n], [n], dim ** -0.5)
+    got = vlm.prompt_attention(q.cuda(), k.cuda(), v.cuda(), [n])
+    U.assert_close(got, o, U.half_step(dtype) * np.abs(o) + 1e-6)

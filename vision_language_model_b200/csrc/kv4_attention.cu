@@ -7,12 +7,14 @@
 // Bound: the codes are read once, 9/8 byte per column and head, so the floor
 // is HBM; what competes with it is the issue rate of turning codes into
 // operands. The layout of the work:
-//   - The G * m query rows of one (sequence, key head) are the 16 rows of
-//     mma.m16n8k16 (fp16 operands, fp32 sums; more rows: further row tiles).
-//     At one to sixteen rows the product is far from the tensor cores' rate,
-//     and its operands can be made in registers, which tcgen05 cannot take.
-//   - A warp takes 16 tokens of a page. Its bytes come by cp.async into a ring
-//     of its own in shared memory, so no warp waits for another.
+//   - The products run as mma.m16n8k16 (fp16 operands, fp32 sums) with the
+//     tokens (S^T = K q^T) and the value columns (O^T = V^T P^T) as the 16 rows
+//     and the G * m query rows of one (sequence, key head) as the 8 columns, two
+//     such tiles for more than 8 rows, further row tiles for more than 16. So
+//     what is made from codes is the big operand, made once in registers, which
+//     tcgen05 cannot take; at these few rows the product is far from its rate.
+//   - A warp takes half pages, 32 tokens, by bulk copies into a ring of its own
+//     in shared memory, so no warp waits for another.
 //   - Code times block scale has at most 6 significant bits, so fp16 holds it
 //     exactly: one cvt and one multiply per two values, no rounding. A query
 //     row is scaled by a power of two so that its largest value lies in [1, 2)
@@ -31,6 +33,8 @@
 // Places behind what a row sees get logit -inf; value scales of places behind
 // the sequence's end are taken as 0, so stale bytes (NaN scales among them)
 // reach no sum. A row that sees nothing is 0.
+#include <cfloat>
+
 #include <algorithm>
 
 #include "kv4.cuh"
@@ -42,28 +46,29 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kSlice = 16;   // tokens of a page per warp
-constexpr int kStages = 4;   // ring of slices per warp
+constexpr int kPart = 32;  // tokens of a page that a warp takes at a time
 constexpr int kMaxSeqs = 4096;  // sequences per launch (their page offsets are held in shared memory)
-constexpr int kCtasPerSm = 3;
+constexpr int kMaxCtasPerSm = 4;
+// registers: O and q take 48 per lane for one 8-row tile, 96 for two
+template <int NT>
+constexpr int kCtasPerSm = NT == 1 ? 4 : 3;
 constexpr int kMinPages = 4;  // a run shorter than this costs more to join than it gains
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNoMax = -3.0e38f;  // a row's maximum before it sees a place; finite, so that -inf minus it is no NaN
 constexpr float kRescale = 8.0f;  // log2 units; P stays below 2^8
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The transpose of an 8 x 8 tile of 16-bit values (row g in lanes 4 g .. 4 g + 3, two columns each).
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -74,7 +79,7 @@ struct Args {
   Kv4 c;
   const void* q;
   int64_t q_stride;  // elements between tokens
-  int heads, group, q_len, rows, row_tiles;
+  int heads, group, q_len, rows, tile_rows, row_tiles;
   float scale;
   void* out;         // [n_seqs * q_len, heads, D]
   int32_t* prefix;   // [n_seqs + 1] page offsets, written by the first kernel's CTA 0
@@ -86,19 +91,24 @@ struct Args {
   int32_t* status;
 };
 
-// Fragment maps. Lane = 4 g + c. The 16 tokens of a slice are the two 8-wide
-// column tiles i of S; column 2 c + e of tile i is token 8 i + 4 e + (c ^ x e).
-// x (1 for D = 128, 2 for D = 64) spreads the rows that one load touches over
-// the banks. A lane's k elements of a query or key row, and its columns of O,
-// are the D / 4 columns from c D / 4 on.
+// Fragment maps. Lane = 4 g + c. Row 8 i + 2 c + e of the 16 tokens of an mma
+// tile is token 8 i + 4 e + (c ^ x e): x (1 for D = 128, 2 for D = 64) spreads
+// the rows that one shared-memory load touches over the banks (the value rows
+// at D = 128 still meet two at a time). As S^T's rows a lane has tokens g and
+// g + 8 (numbered so), as V^T's columns tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9.
+// A lane's elements of key and query rows are the D / 4 columns from c D / 4 on,
+// its value columns (rows of O^T) the D / 8 from g D / 8 on, its query rows (the
+// mma columns of S^T and O^T) 2 c and 2 c + 1 of each 8-row tile.
 template <int D>
 struct Map {
   static constexpr int kX = D == 128 ? 1 : 2;
-  static constexpr int kSteps = D / 16;                // mma steps of a logit
-  static constexpr int kCols = D / 4;                  // columns per lane
-  static constexpr int kKOff = 0, kVOff = kSlice * D / 2;
-  static constexpr int kKsOff = kSlice * D, kVsOff = kKsOff + kSlice * D / 16;
-  static constexpr int kBytes = kVsOff + kSlice * D / 16;  // one slice
+  static constexpr int kSteps = D / 16;  // mma steps of a logit
+  static constexpr int kCols = D / 4;    // columns per lane
+  // a ring slot: 32 tokens as key codes, value codes, key scales, value scales
+  static constexpr int kV = kPart * D / 2, kKs = 2 * kV, kVs = kKs + kPart * D / 16;
+  static constexpr int kBytes = kVs + kPart * D / 16;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kRing = kStages * kBytes;  // bytes per warp
   static __device__ __forceinline__ int token(int i, int c, int e) { return 8 * i + 4 * e + (c ^ (kX * e)); }
 };
 
@@ -135,16 +145,16 @@ __device__ __forceinline__ Plan make_plan(const Kv4& c, int units_per_seq, int g
   return p;
 }
 
-// A lane's part of the 16 query rows [first, first + 16) of (sequence, key
-// head) as mma A fragments, and the factor of its two rows' logits.
-template <typename T, int D>
-__device__ __forceinline__ void load_q(const Args& a, int s, int kvh, int first, uint32_t (&qf)[D / 16][4],
-                                       float (&factor)[2]) {
+// The query rows [first, first + 8 NT) of (sequence, key head) as mma B
+// fragments, and the factors of the logits of the lane's rows 2 c, 2 c + 1.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void load_q(const Args& a, int s, int kvh, int first, uint32_t (&qf)[NT][D / 16][2],
+                                       float (&factor)[NT][2]) {
   using M = Map<D>;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int r = first + g + 8 * half;
+  for (int n = 0; n < NT; ++n) {
+    const int r = first + 8 * n + g;
     uint32_t w[M::kCols / 2];
 #pragma unroll
     for (int j = 0; j < M::kCols / 2; ++j) w[j] = 0;
@@ -169,71 +179,101 @@ __device__ __forceinline__ void load_q(const Args& a, int s, int kvh, int first,
     // 2^-floor(log2 amax); 1 where amax is 0, subnormal or infinite
     const int e = static_cast<int>(__float_as_uint(amax) >> 23);
     const float mul = e == 0 || e == 255 ? 1.0f : __uint_as_float(static_cast<uint32_t>(max(254 - e, 1)) << 23);
-    factor[half] = a.scale * a.c.k_sg * kLog2e / mul;
+    const float mine = fmaxf(a.scale * a.c.k_sg * kLog2e / mul, FLT_MIN);  // not 0: it multiplies -inf
+    factor[n][0] = __shfl_sync(0xffffffffu, mine, 8 * c);
+    factor[n][1] = __shfl_sync(0xffffffffu, mine, 8 * c + 4);
 #pragma unroll
     for (int k = 0; k < M::kSteps; ++k) {
       const float2 f0 = unpack16<T>(w[2 * k]), f1 = unpack16<T>(w[2 * k + 1]);
-      qf[k][half] = pack_f16x2(f0.x * mul, f0.y * mul);
-      qf[k][2 + half] = pack_f16x2(f1.x * mul, f1.y * mul);
+      qf[n][k][0] = pack_f16x2(f0.x * mul, f0.y * mul);
+      qf[n][k][1] = pack_f16x2(f1.x * mul, f1.y * mul);
     }
   }
 }
 
-// A warp's 16 tokens of one page into its ring slot (keys only: kValues false).
-template <int D, bool kValues>
-__device__ __forceinline__ void fetch(uint32_t dst, const uint8_t* page, int warp) {
-  using L = Kv4Layout<D>;
-  using M = Map<D>;
-  const int lane = threadIdx.x & 31;
-  const uint8_t* k = page + warp * kSlice * L::kCodeRow;
-  const uint8_t* v = page + L::kV + warp * kSlice * L::kCodeRow;
-  constexpr int kPerRow = D / 32;  // 16-byte chunks of a code row
-#pragma unroll
-  for (int j = 0; j < kSlice * kPerRow / 32; ++j) {
-    const int x = j * 32 + lane, row = x / kPerRow, ch = x % kPerRow;
-    cp_async16(dst + M::kKOff + x * 16, k + x * 16);
-    // the value rows' chunks are exchanged by row so that four rows' halves lie in different banks (D = 128)
-    if (kValues) cp_async16(dst + M::kVOff + (row * kPerRow + (D == 128 ? ch ^ (row & 2) : ch)) * 16, v + x * 16);
-  }
-  constexpr int kSc = kSlice * D / 256;  // 16-byte chunks of a slice's scales
-  if (lane < kSc)
-    cp_async16(dst + M::kKsOff + lane * 16, page + L::kKs + warp * kSlice * L::kScaleRow + lane * 16);
-  else if (kValues && lane < 2 * kSc)
-    cp_async16(dst + M::kVsOff + (lane - kSc) * 16,
-               page + L::kVs + warp * kSlice * L::kScaleRow + (lane - kSc) * 16);
-}
-
-// S = q . (code * scale) for the 16 tokens of a slice.
+// The halves of a run's pages that a warp takes, every kWarps-th, through its
+// ring: four bulk copies each, one by each of the lanes 0..3, counted on one
+// barrier. All lanes call together. kWarps is even, so a warp takes the same
+// half of every page and a copy's place inside the page never changes.
 template <int D>
-__device__ __forceinline__ void logits(const uint8_t* st, const uint32_t (&qf)[D / 16][4], float (&s)[2][4]) {
+struct PartRing {
+  static_assert(kWarps % 2 == 0, "one half per warp");
+  uint32_t bars;        // shared-memory address of the barriers
+  uint32_t dst, bytes;  // this lane's copy: into slot 0, its size
+  uint32_t src;         // its offset in a page
+  uint32_t issued = 0, taken = 0;
+  __device__ __forceinline__ PartRing(uint32_t ring, uint32_t bars_, int half, int lane) : bars(bars_) {
+    using M = Map<D>;
+    using L = Kv4Layout<D>;
+    const int which = lane & 1;
+    const bool codes = (lane & 2) == 0;
+    bytes = codes ? M::kV : M::kVs - M::kKs;
+    src = codes ? which * L::kV + half * M::kV : L::kKs + which * (L::kVs - L::kKs) + half * (M::kVs - M::kKs);
+    dst = ring + (codes ? which * M::kV : M::kKs + which * (M::kVs - M::kKs));
+  }
+  __device__ __forceinline__ void issue(const uint8_t* page, int lane) {
+    using M = Map<D>;
+    const uint32_t st = issued % M::kStages, bar = bars + st * 8;
+    if (lane == 0) mbar_arrive_expect_tx(bar, M::kBytes);
+    __syncwarp();
+    if (lane < 4)
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                       dst + st * M::kBytes),
+                   "l"(page + src), "r"(bytes), "r"(bar)
+                   : "memory");
+    ++issued;
+  }
+  __device__ __forceinline__ bool wait(volatile int* abort, int32_t* status) const {
+    constexpr uint32_t n = Map<D>::kStages;
+    return mbar_wait_warp(bars + taken % n * 8, (taken / n) & 1, abort, status);
+  }
+};
+
+// S^T = (code * scale) . q for the 32 tokens of a ring slot: s[x][n] is 16
+// tokens by 8 query rows.
+template <int D, int NT>
+__device__ __forceinline__ void logits(const uint8_t* part, const uint32_t (&qf)[NT][D / 16][2], float (&s)[2][NT][4]) {
   using M = Map<D>;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int x = 0; x < 2; ++x) {
+    uint32_t w[2][D / 32], sc[2][D == 128 ? 2 : 1];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
-    const int row = M::token(i, g >> 1, g & 1);
-    uint32_t w[D / 32];
-    uint32_t sc[2];
-    if constexpr (D == 128) {
-      const uint4 u = *reinterpret_cast<const uint4*>(st + M::kKOff + row * 64 + c * 16);
-      w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-      const uint32_t h2 = e4m3x2_f16(*reinterpret_cast<const uint16_t*>(st + M::kKsOff + row * 8 + 2 * c));
-      sc[0] = __byte_perm(h2, 0, 0x1010);
-      sc[1] = __byte_perm(h2, 0, 0x3232);
-    } else {
-      const uint2 u = *reinterpret_cast<const uint2*>(st + M::kKOff + row * 32 + c * 8);
-      w[0] = u.x; w[1] = u.y;
-      const uint32_t h2 = e4m3x2_f16(st[M::kKsOff + row * 4 + c]);
-      sc[0] = sc[1] = __byte_perm(h2, 0, 0x1010);
+    for (int i = 0; i < 2; ++i) {
+      const int row = 16 * x + M::token(i, g >> 1, g & 1);
+      if constexpr (D == 128) {
+        const uint4 u = *reinterpret_cast<const uint4*>(part + row * 64 + c * 16);
+        w[i][0] = u.x; w[i][1] = u.y; w[i][2] = u.z; w[i][3] = u.w;
+        const uint32_t h2 = e4m3x2_f16(*reinterpret_cast<const uint16_t*>(part + M::kKs + row * 8 + 2 * c));
+        sc[i][0] = __byte_perm(h2, 0, 0x1010);
+        sc[i][1] = __byte_perm(h2, 0, 0x3232);
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(part + row * 32 + c * 8);
+        w[i][0] = u.x; w[i][1] = u.y;
+        const uint32_t h2 = e4m3x2_f16(part[M::kKs + row * 4 + c]);
+        sc[i][0] = __byte_perm(h2, 0, 0x1010);
+      }
     }
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) {
-      uint32_t p[4];
-      e2m1x8_f16(w[x], p);
-      const uint32_t f = sc[D == 128 ? x >> 1 : 0];
-      mma16816(s[i], qf[2 * x], hmul2(p[0], f), hmul2(p[1], f));
-      mma16816(s[i], qf[2 * x + 1], hmul2(p[2], f), hmul2(p[3], f));
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[x][n][j] = 0.0f;
+#pragma unroll
+    for (int y = 0; y < D / 32; ++y) {
+      uint32_t p[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        e2m1x8_f16(w[i][y], p[i]);
+        const uint32_t f = sc[i][D == 128 ? y >> 1 : 0];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[i][j] = hmul2(p[i][j], f);
+      }
+      const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]}, a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma16816(s[x][n], a0, qf[n][2 * y][0], qf[n][2 * y][1]);
+        mma16816(s[x][n], a1, qf[n][2 * y + 1][0], qf[n][2 * y + 1][1]);
+      }
     }
   }
 }
@@ -261,11 +301,11 @@ __device__ __forceinline__ Place place_of(const int* prefix, int n_seqs, int kv_
 }
 
 // Element (row, column quad) of the O tile a warp leaves in its ring, in
-// floats; the exchange spreads the quads of a column group over the banks.
+// floats; the exchange spreads the rows that one store touches over the banks.
 template <int D>
 __device__ __forceinline__ int o_at(int row, int quad) {
-  constexpr int kPer = D / 16;  // quads per lane's column run
-  return row * D + ((quad ^ ((quad / kPer) * 2) ^ (row & 1)) * 4);
+  const int c = row >> 1;
+  return row * D + ((quad ^ (D == 128 ? c & 3 : (c & 1) | ((c & 2) << 1))) * 4);
 }
 
 template <typename T>
@@ -273,19 +313,148 @@ __device__ __forceinline__ void store4(T* dst, float x, float y, float z, float 
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<T>(x, y), pack16<T>(z, w));
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Args a) {
+// A lane's running state of its query rows 2 c and 2 c + 1 of each tile: O, the
+// rows' maxima (of the products, before `factor`: a rounded product would not do
+// for large ones) and its part of their sums.
+template <int D, int NT>
+struct State {
+  float o[NT][D / 16][4];
+  float m[NT][2], grow[NT][2];  // the maximum moves when a product passes `grow`, kRescale above it in log2 units
+  uint64_t l[NT];
+};
+
+// The 32 tokens of a ring slot, from place `first` on, into the state.
+template <int D, int NT, bool kEdge>
+__device__ __forceinline__ void take32(const uint8_t* part, int first, int len, const int (&seen)[NT][2],
+                                       const uint32_t (&qf)[NT][D / 16][2], const float (&factor)[NT][2],
+                                       State<D, NT>& z) {
+  using M = Map<D>;
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  float s[2][NT][4];
+  logits<D, NT>(part, qf, s);
+  if (kEdge) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = first + 16 * x + M::token(e >> 1, g >> 1, g & 1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          if (j >= seen[n][e & 1]) s[x][n][e] = -INFINITY;
+      }
+  }
+  bool grows = false;
+  float mx[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      mx[n][r] = fmaxf(max3f(s[0][n][r], s[0][n][2 + r], s[1][n][r]), s[1][n][2 + r]);
+      grows |= mx[n][r] > z.grow[n][r];
+    }
+  if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float corr[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float v = mx[n][r];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        v = fmaxf(v, z.m[n][r]);
+        corr[r] = ex2((z.m[n][r] - v) * factor[n][r]);
+        z.m[n][r] = v;
+        z.grow[n][r] = v + kRescale / factor[n][r];
+      }
+      z.l[n] = mul2(z.l[n], pack2(__float_as_uint(corr[0]), __float_as_uint(corr[1])));
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z.o[n][j][e] *= corr[e & 1];
+    }
+  }
+  uint32_t pf[2][NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const uint64_t f2 = pack2(__float_as_uint(factor[n][0]), __float_as_uint(factor[n][1]));
+    const uint64_t negm = pack2(__float_as_uint(-z.m[n][0]), __float_as_uint(-z.m[n][1]));
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x0, x1;
+        unpack2(mul2(add2(pack2(__float_as_uint(s[x][n][2 * i]), __float_as_uint(s[x][n][2 * i + 1])), negm), f2), x0, x1);
+        x0 = ex2(x0);
+        x1 = ex2(x1);
+        z.l[n] = add2(z.l[n], pack2(__float_as_uint(x0), __float_as_uint(x1)));
+        pf[x][n][i] = transpose8(pack_f16x2(x0, x1));
+      }
+  }
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    uint32_t vsc[2], v[2][2][D / 64];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t by[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 16 * x + M::token(i, c, e);
+        by[e] = D == 128 ? part[M::kVs + row * 8 + g] : part[M::kVs + row * 4 + (g >> 1)];
+        if (kEdge && first + row >= len) by[e] = 0;
+        if constexpr (D == 128) {
+          const uint2 u = *reinterpret_cast<const uint2*>(part + M::kV + row * 64 + 8 * g);
+          v[i][e][0] = u.x;
+          v[i][e][1] = u.y;
+        } else {
+          v[i][e][0] = *reinterpret_cast<const uint32_t*>(part + M::kV + row * 32 + 4 * g);
+        }
+      }
+      vsc[i] = e4m3x2_f16(by[0] | by[1] << 8);
+    }
+#pragma unroll
+    for (int w = 0; w < D / 64; ++w) {
+      // the two tokens' codes of one column side by side before they are converted:
+      // even columns in y[i][0], odd ones in y[i][1]
+      uint32_t y[2][2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        constexpr uint32_t m = 0x0F0F0F0Fu;
+        e2m1x8_f16((v[i][0][w] & m) | ((v[i][1][w] << 4) & ~m), y[i][0]);
+        e2m1x8_f16(((v[i][0][w] >> 4) & m) | (v[i][1][w] & ~m), y[i][1]);
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        // columns g D / 8 + 8 w + 2 b (rows g of the tile) and + 1 (rows g + 8)
+        const uint32_t at[4] = {hmul2(y[0][0][b], vsc[0]), hmul2(y[0][1][b], vsc[0]), hmul2(y[1][0][b], vsc[1]),
+                                hmul2(y[1][1][b], vsc[1])};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16816(z.o[n][4 * w + b], at, pf[x][n][0], pf[x][n][1]);
+      }
+    }
+  }
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) kv4_attn_kernel(const Args a) {
   using M = Map<D>;
   using L = Kv4Layout<D>;
-  static_assert(kStages * M::kBytes >= 16 * D * 4, "a warp's O tile fits its ring");
-  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kTileRows = 8 * NT;
+  static_assert(M::kRing >= kTileRows * D * 4, "a warp's O tile fits its ring");
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int warp_sum[kWarps];
-  __shared__ float sm_m[kWarps][16], sm_l[kWarps][16];
-  uint8_t* ring_base = smem;
-  int* prefix = reinterpret_cast<int*>(smem + kWarps * kStages * M::kBytes);
+  __shared__ float sm_m[kWarps][kTileRows], sm_l[kWarps][kTileRows];
+  __shared__ uint64_t bars[kWarps][M::kStages];
+  __shared__ int abort_flag;
+  int* prefix = reinterpret_cast<int*>(smem + kWarps * M::kRing);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  uint8_t* ring = ring_base + warp * kStages * M::kBytes;
-  const uint32_t ring_s = smem_u32(ring);
+  uint8_t* ring = smem + warp * M::kRing;
+  PartRing<D> pr(smem_u32(ring), smem_u32(bars[warp]), warp & 1, lane);
+  if (lane == 0) {
+    for (int i = 0; i < M::kStages; ++i) mbar_init(smem_u32(&bars[warp][i]), 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 0) abort_flag = 0;
+  volatile int* abort_v = &abort_flag;
 
   griddep_wait();
   griddep_launch_dependents();
@@ -301,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Ar
     for (int i = threadIdx.x; i < a.q_len * a.heads * D / 4; i += kThreads) dst[i] = make_uint2(0, 0);
   }
 
+  bool ok = true;
   const int64_t begin = blockIdx.x * plan.chunk;
   const int64_t end = min(plan.total, begin + plan.chunk);
   for (int64_t x = begin; x < end;) {
@@ -308,161 +478,101 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Ar
     const int p0 = at.page;
     const int p1 = static_cast<int>(min(static_cast<int64_t>(at.pages), p0 + (end - x)));
     const int len = kv4_len(a.c, at.s, nullptr);
+
+    // this warp's half pages 2 p0 + warp, + kWarps, ...: two of kWarps = 4 pages' eight;
+    // the page numbers of the next 32 of them, one per lane
+    const int mine = (2 * (p1 - p0) - warp + kWarps - 1) / kWarps;
+    int ids = 0;
+    auto issue = [&](int k) {  // k in order, all lanes together
+      if (k % 32 == 0) {
+        const int e = p0 + (warp + (k + lane) * kWarps) / 2;
+        ids = e < p1 ? static_cast<int>(kv4_page(a.c, at.s, e, a.status)) : 0;
+      }
+      pr.issue(a.c.pages + (static_cast<int64_t>(__shfl_sync(0xffffffffu, ids, k % 32)) * a.c.kv_heads + at.kvh) * L::kBytes,
+               lane);
+    };
+    int next = 0;
+    for (; next < min(mine, M::kStages); ++next) issue(next);
+
     // the places below `open` are seen by every row
     const int open = len - a.q_len + 1;
-    uint32_t qf[D / 16][4];
-    float factor[2];
-    load_q<T, D>(a, at.s, at.kvh, at.tile * 16, qf, factor);
-    int seen[2];  // one past the last place each of the lane's rows sees
+    uint32_t qf[NT][M::kSteps][2];
+    float factor[NT][2];
+    load_q<T, D, NT>(a, at.s, at.kvh, at.tile * kTileRows, qf, factor);
+    int seen[NT][2];  // one past the last place each of the lane's rows sees
+    State<D, NT> z;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) seen[half] = open + (at.tile * 16 + g + 8 * half) / a.group;
-
-    float o[D / 8][4];
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-
-    int ids = 0, ids_at = p0;  // page offsets of 32 entries from ids_at on, one per lane
-    auto issue = [&](int p) {
-      if (p < p1) {
-        if (p >= ids_at + 32 || p == p0) {
-          ids_at = p;
-          ids = p + lane < p1 ? static_cast<int>(kv4_page(a.c, at.s, p + lane, a.status)) : 0;
-        }
-        const int id = __shfl_sync(0xffffffffu, ids, p - ids_at);
-        if (p * kKv4Page + warp * kSlice < len)
-          fetch<D, true>(ring_s + (p - p0) % kStages * M::kBytes,
-                         a.c.pages + (static_cast<int64_t>(id) * a.c.kv_heads + at.kvh) * L::kBytes, warp);
+      for (int r = 0; r < 2; ++r) {
+        seen[n][r] = open + (at.tile * kTileRows + 8 * n + 2 * c + r) / a.group;
+        z.m[n][r] = z.grow[n][r] = kNoMax;
       }
-      cp_async_commit();
-    };
+      z.l[n] = 0;
 #pragma unroll
-    for (int j = 0; j < kStages - 1; ++j) issue(p0 + j);
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z.o[n][j][e] = 0.0f;
+    }
 
-    for (int p = p0; p < p1; ++p) {
-      cp_async_wait<kStages - 2>();
+    for (int k = 0; k < mine; ++k) {
+      if (ok) ok = pr.wait(abort_v, a.status);
+      const uint8_t* part = ring + pr.taken % M::kStages * M::kBytes;
+      const int first = p0 * kKv4Page + (warp + k * kWarps) * kPart;
+      if (ok) {
+        if (first + kPart <= open)
+          take32<D, NT, false>(part, first, len, seen, qf, factor, z);
+        else
+          take32<D, NT, true>(part, first, len, seen, qf, factor, z);
+      }
+      ++pr.taken;
       __syncwarp();
-      const uint8_t* st = ring + (p - p0) % kStages * M::kBytes;
-      issue(p + kStages - 1);
-      const int first = p * kKv4Page + warp * kSlice;
-      if (first >= len) continue;
-      float s[2][4];
-      logits<D>(st, qf, s);
-      float mx[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][e] *= factor[e >> 1];
-      const bool edge = first + kSlice > open;
-      if (edge) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (first + M::token(i, c, e & 1) >= seen[e >> 1]) s[i][e] = -INFINITY;
-      }
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-        mx[half] = fmaxf(fmaxf(s[0][2 * half], s[0][2 * half + 1]), fmaxf(s[1][2 * half], s[1][2 * half + 1]));
-      if (__any_sync(0xffffffffu, mx[0] > m[0] + kRescale || mx[1] > m[1] + kRescale)) {
-        float corr[2];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float v = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 1));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-          v = fmaxf(v, m[half]);
-          corr[half] = v == m[half] ? 1.0f : ex2(m[half] - v);
-          m[half] = v;
-          l[half] *= corr[half];
-        }
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[j][e] *= corr[e >> 1];
-      }
-      uint32_t pf[4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float ref = m[half] == -INFINITY ? 0.0f : m[half];
-          const float x0 = ex2(s[i][2 * half] - ref), x1 = ex2(s[i][2 * half + 1] - ref);
-          l[half] += x0 + x1;
-          pf[2 * i + half] = pack_f16x2(x0, x1);
-        }
-      // values: token pairs (2 c, 2 c + 1) of each column tile, columns g D / 8 + j
-      uint32_t vsc[2], v[2][2][D / 64];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t by[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = M::token(i, c, e);
-          by[e] = D == 128 ? st[M::kVsOff + row * 8 + g] : st[M::kVsOff + row * 4 + (g >> 1)];
-          if (edge && first + row >= len) by[e] = 0;
-          if constexpr (D == 128) {
-            const uint2 u = *reinterpret_cast<const uint2*>(st + M::kVOff + row * 64 + ((8 * g) ^ ((row & 2) * 16)));
-            v[i][e][0] = u.x;
-            v[i][e][1] = u.y;
-          } else {
-            v[i][e][0] = *reinterpret_cast<const uint32_t*>(st + M::kVOff + row * 32 + 4 * g);
-          }
-        }
-        vsc[i] = e4m3x2_f16(by[0] | by[1] << 8);
-      }
-#pragma unroll
-      for (int w = 0; w < D / 64; ++w) {
-        uint32_t x[2][2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) e2m1x8_f16(v[i][e][w], x[i][e]);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          mma16816(o[8 * w + 2 * b], pf, hmul2(__byte_perm(x[0][0][b], x[0][1][b], 0x5410), vsc[0]),
-                   hmul2(__byte_perm(x[1][0][b], x[1][1][b], 0x5410), vsc[1]));
-          mma16816(o[8 * w + 2 * b + 1], pf, hmul2(__byte_perm(x[0][0][b], x[0][1][b], 0x7632), vsc[0]),
-                   hmul2(__byte_perm(x[1][0][b], x[1][1][b], 0x7632), vsc[1]));
-        }
+      if (ok && next < mine) {
+        issue(next);
+        ++next;
       }
     }
-    cp_async_wait<0>();
-
-    // join the four warps: a common maximum per row, each warp's O in its ring
+    // join the four warps: a common maximum per row (in log2 units), each warp's O in its ring
+    float m[NT][2];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
-      l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
-      if (c == 0) {
-        sm_m[warp][g + 8 * half] = m[half];
-        sm_l[warp][g + 8 * half] = l[half];
+    for (int n = 0; n < NT; ++n) {
+      float l[2];
+      unpack2(z.l[n], l[0], l[1]);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+        m[n][r] = z.m[n][r] == kNoMax ? -INFINITY : z.m[n][r] * factor[n][r];
+        if (g == 0) {
+          sm_m[warp][8 * n + 2 * c + r] = m[n][r];
+          sm_l[warp][8 * n + 2 * c + r] = l[r];
+        }
       }
     }
     __syncthreads();
     float* own = reinterpret_cast<float*>(ring);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int r = g + 8 * half;
-      float top = sm_m[0][r];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm_m[w][r]);
-      const float f = m[half] == top ? 1.0f : ex2(m[half] - top);
-      // column c D / 4 + y is element 2 (y / (D / 8)) + ... : tile y % (D / 8), pair member y / (D / 8)
+      for (int r = 0; r < 2; ++r) {
+        const int row = 8 * n + 2 * c + r;
+        float top = sm_m[0][row];
 #pragma unroll
-      for (int y = 0; y < D / 4; y += 4) {
-        const int e = 2 * half + y / (D / 8), j = y % (D / 8);
-        *reinterpret_cast<float4*>(own + o_at<D>(r, c * (D / 16) + y / 4)) =
-            make_float4(o[j][e] * f, o[j + 1][e] * f, o[j + 2][e] * f, o[j + 3][e] * f);
+        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm_m[w][row]);
+        const float f = m[n][r] == top ? 1.0f : ex2(m[n][r] - top);
+        // columns g D / 8 + 2 j (elements r) and + 1 (elements 2 + r) of tile j
+#pragma unroll
+        for (int j = 0; j < D / 16; j += 2)
+          *reinterpret_cast<float4*>(own + o_at<D>(row, g * (D / 32) + j / 2)) =
+              make_float4(z.o[n][j][r] * f, z.o[n][j][2 + r] * f, z.o[n][j + 1][r] * f, z.o[n][j + 1][2 + r] * f);
       }
-    }
     __syncthreads();
     const bool whole = p0 == 0 && p1 == at.pages;
     const int slot = 2 * blockIdx.x + (x == begin ? 0 : 1);
     {
-      const int r = threadIdx.x >> 3, part = threadIdx.x & 7;  // 16 rows, 8 threads each
-      const int row = at.tile * 16 + r;
+      constexpr int kPer = kThreads / kTileRows;  // threads per row
+      const int r = threadIdx.x / kPer, part = threadIdx.x % kPer;
+      const int row = at.tile * kTileRows + r;
       if (row < a.rows) {
         float top = sm_m[0][r], sum = 0.0f;
 #pragma unroll
@@ -473,13 +583,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Ar
         T* dst = static_cast<T*>(a.out) +
                  ((static_cast<int64_t>(at.s) * a.q_len + row / a.group) * a.heads + at.kvh * a.group + row % a.group) * D;
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          const int quad = part + 8 * k;
+        for (int k = 0; k < D / 4 / kPer; ++k) {
+          const int quad = part + kPer * k;
           float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
             const float4 u = *reinterpret_cast<const float4*>(
-                reinterpret_cast<const float*>(ring_base + w * kStages * M::kBytes) + o_at<D>(r, quad));
+                reinterpret_cast<const float*>(smem + w * M::kRing) + o_at<D>(r, quad));
             t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
           }
           if (whole)
@@ -495,6 +605,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Ar
         }
       }
     }
+    fence_proxy_async_smem();  // the O tiles were written where the next pages will be copied
     __syncthreads();
     x += p1 - p0;
   }
@@ -509,7 +620,7 @@ __global__ void __launch_bounds__(kThreads) kv4_combine_kernel(const Args a) {
   __shared__ float sm_o[kWarps][D];
   __shared__ float2 sm_ml[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.y, tile = row / 16, r = row % 16;
+  const int row = blockIdx.y, tile = row / a.tile_rows, r = row % a.tile_rows;
   const int s = blockIdx.x / a.c.kv_heads, kvh = blockIdx.x % a.c.kv_heads;
   const int per_seq = a.c.kv_heads * a.row_tiles;
   const int64_t total = static_cast<int64_t>(a.prefix[a.c.n_seqs]) * per_seq;
@@ -568,16 +679,25 @@ __global__ void __launch_bounds__(kThreads) kv4_combine_kernel(const Args a) {
 // more from the keys alone (half the cache's bytes; storing them in the first
 // kernel would cost 8 bytes per row and token). One warp owns a slice and sums
 // its rows in a fixed order, so no atomics.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) kv4_weights_kernel(const Args a) {
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) kv4_weights_kernel(const Args a) {
   using M = Map<D>;
   using L = Kv4Layout<D>;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int warp_sum[kWarps];
-  int* prefix = reinterpret_cast<int*>(smem + kWarps * kStages * M::kBytes);
+  __shared__ uint64_t bars[kWarps][M::kStages];
+  __shared__ int abort_flag;
+  int* prefix = reinterpret_cast<int*>(smem + kWarps * M::kRing);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  uint8_t* ring = smem + warp * kStages * M::kBytes;
-  const uint32_t ring_s = smem_u32(ring);
+  uint8_t* ring = smem + warp * M::kRing;
+  PartRing<D> pr(smem_u32(ring), smem_u32(bars[warp]), warp & 1, lane);
+  if (lane == 0) {
+    for (int i = 0; i < M::kStages; ++i) mbar_init(smem_u32(&bars[warp][i]), 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 0) abort_flag = 0;
+  volatile int* abort_v = &abort_flag;
+  bool ok = true;
   griddep_wait();
   griddep_launch_dependents();
   const Plan plan = make_plan(a.c, a.c.kv_heads, gridDim.x, prefix, warp_sum, nullptr);
@@ -591,82 +711,101 @@ __global__ void __launch_bounds__(kThreads) kv4_weights_kernel(const Args a) {
     const int open = len - a.q_len + 1;
     const float* lse = a.lse + (static_cast<int64_t>(at.s) * a.c.kv_heads + at.kvh) * a.rows;
     float* dst = a.weights + (static_cast<int64_t>(at.s) * a.c.kv_heads + at.kvh) * a.c.max_pages * kKv4Page;
-    uint32_t qf[D / 16][4];
-    float factor[2], norm[2];
+    uint32_t qf[NT][M::kSteps][2];
+    float factor[NT][2], norm[NT][2];
+    int seen[NT][2];
     auto rows_of = [&](int tile) {
-      load_q<T, D>(a, at.s, at.kvh, tile * 16, qf, factor);
+      load_q<T, D, NT>(a, at.s, at.kvh, tile * 8 * NT, qf, factor);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int row = tile * 16 + g + 8 * half;
-        norm[half] = row < a.rows ? lse[row] : INFINITY;
-      }
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = tile * 8 * NT + 8 * n + 2 * c + r;
+          norm[n][r] = row < a.rows ? lse[row] : INFINITY;
+          seen[n][r] = row < a.rows ? open + row / a.group : 0;
+        }
     };
     rows_of(0);
-    int ids = 0, ids_at = p0;
-    auto issue = [&](int p) {
-      if (p < p1) {
-        if (p >= ids_at + 32 || p == p0) {
-          ids_at = p;
-          ids = p + lane < p1 ? static_cast<int>(kv4_page(a.c, at.s, p + lane, a.status)) : 0;
-        }
-        const int id = __shfl_sync(0xffffffffu, ids, p - ids_at);
-        if (p * kKv4Page + warp * kSlice < len)
-          fetch<D, false>(ring_s + (p - p0) % kStages * M::kBytes,
-                          a.c.pages + (static_cast<int64_t>(id) * a.c.kv_heads + at.kvh) * L::kBytes, warp);
+    const int mine = (2 * (p1 - p0) - warp + kWarps - 1) / kWarps;
+    int ids = 0;
+    auto issue = [&](int k) {
+      if (k % 32 == 0) {
+        const int e = p0 + (warp + (k + lane) * kWarps) / 2;
+        ids = e < p1 ? static_cast<int>(kv4_page(a.c, at.s, e, a.status)) : 0;
       }
-      cp_async_commit();
+      pr.issue(a.c.pages + (static_cast<int64_t>(__shfl_sync(0xffffffffu, ids, k % 32)) * a.c.kv_heads + at.kvh) * L::kBytes,
+               lane);
     };
+    int next = 0;
+    for (; next < min(mine, M::kStages); ++next) issue(next);
+    for (int k = 0; k < mine; ++k) {
+      if (ok) ok = pr.wait(abort_v, a.status);
+      const uint8_t* part = ring + pr.taken % M::kStages * M::kBytes;
+      const int first = p0 * kKv4Page + (warp + k * kWarps) * kPart;
+      if (ok && first < len) {
+        float w[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // tokens g and g + 8 of both tiles
+        for (int tile = 0; tile < a.row_tiles; ++tile) {
+          if (a.row_tiles > 1) rows_of(tile);
+          float s[2][NT][4];
+          logits<D, NT>(part, qf, s);
 #pragma unroll
-    for (int j = 0; j < kStages - 1; ++j) issue(p0 + j);
-    for (int p = p0; p < p1; ++p) {
-      cp_async_wait<kStages - 2>();
-      __syncwarp();
-      const uint8_t* st = ring + (p - p0) % kStages * M::kBytes;
-      issue(p + kStages - 1);
-      const int first = p * kKv4Page + warp * kSlice;
-      if (first >= len) continue;
-      float w[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // [column tile][pair member]
-      for (int tile = 0; tile < a.row_tiles; ++tile) {
-        if (a.row_tiles > 1) rows_of(tile);
-        float s[2][4];
-        logits<D>(st, qf, s);
+          for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+            for (int e = 0; e < 4; ++e) {
+              const int j = first + 16 * x + M::token(e >> 1, g >> 1, g & 1);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int half = e >> 1;
-            const int row = tile * 16 + g + 8 * half;
-            const bool sees = first + M::token(i, c, e & 1) < open + row / a.group;
-            const float p2 = ex2(s[i][e] * factor[half] - norm[half]);
-            w[i][e & 1] += sees && row < a.rows ? p2 : 0.0f;
+              for (int n = 0; n < NT; ++n) {
+                const float p2 = ex2(__fmul_rn(s[x][n][e], factor[n][e & 1]) - norm[n][e & 1]);
+                w[x][e >> 1] += j < seen[n][e & 1] ? p2 : 0.0f;
+              }
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float v = w[x][i];
+            v += __shfl_xor_sync(0xffffffffu, v, 1);
+            v += __shfl_xor_sync(0xffffffffu, v, 2);
+            const int j = first + 16 * x + M::token(i, g >> 1, g & 1);
+            if (c == 2 * x + i && j < len) dst[j] += v;
           }
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float v = w[i][e];
-          v += __shfl_xor_sync(0xffffffffu, v, 4);
-          v += __shfl_xor_sync(0xffffffffu, v, 8);
-          v += __shfl_xor_sync(0xffffffffu, v, 16);
-          const int j = first + M::token(i, c, e);
-          if (g == 0 && j < len) dst[j] += v;
-        }
+      ++pr.taken;
+      __syncwarp();
+      if (ok && next < mine) {
+        issue(next);
+        ++next;
+      }
     }
-    cp_async_wait<0>();
-    __syncwarp();
     x += p1 - p0;
   }
 }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
+// Opts the kernels in to their shared memory (static parts included, more than
+// 48 KB), once per device.
+template <typename T, int D, int NT>
+bool smem_ready() {
+  static bool done[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev < 64 && done[dev]) return true;
+  constexpr int most = kWarps * Map<D>::kRing + (kMaxSeqs + 1) * 4;
+  if (cudaFuncSetAttribute(kv4_attn_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+      cudaFuncSetAttribute(kv4_weights_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+    return false;
+  if (dev < 64) done[dev] = true;
+  return true;
+}
+
 }  // namespace
 
 size_t kv4_attention_workspace(int n_seqs, int heads, int kv_heads, int head_dim, int q_len) {
   (void)kv_heads;
   const size_t n = std::min(n_seqs, kMaxSeqs);
-  const size_t slots = 2 * static_cast<size_t>(kCtasPerSm) * 256;  // 256: above any SM count
+  const size_t slots = 2 * static_cast<size_t>(kMaxCtasPerSm) * 256;  // 256: above any SM count
   return up((n + 1) * 4) + up(slots * 16 * head_dim * 4) + up(slots * 16 * 8) + up(n * heads * q_len * 4);
 }
 
@@ -678,11 +817,14 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
   a.group = heads / c0.kv_heads;
   a.q_len = q_len;
   a.rows = a.group * q_len;
-  a.row_tiles = (a.rows + 15) / 16;
+  // one 8-row tile holds the rows, or tiles of 16 (two of 8 that share the operand made from codes)
+  const bool one = a.rows <= 8;
+  a.tile_rows = one ? 8 : 16;
+  a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
   a.scale = scale;
-  a.grid = kCtasPerSm * std::min(num_sms(), 256);
+  a.grid = (one ? kCtasPerSm<1> : kCtasPerSm<2>) * std::min(num_sms(), 256);
   a.status = status;
-  const size_t slots = 2 * static_cast<size_t>(kCtasPerSm) * 256;
+  const size_t slots = 2 * static_cast<size_t>(kMaxCtasPerSm) * 256;
   const int n_max = std::min(c0.n_seqs, kMaxSeqs);
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.prefix = reinterpret_cast<int32_t*>(w);
@@ -692,14 +834,10 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
   a.part_ml = reinterpret_cast<float2*>(w);
   w += up(slots * 16 * 8);
   a.lse = weights == nullptr ? nullptr : reinterpret_cast<float*>(w);
-  const size_t smem = kWarps * kStages * (head_dim == 128 ? Map<128>::kBytes : Map<64>::kBytes) +
+  const size_t smem = kWarps * (head_dim == 128 ? Map<128>::kRing : Map<64>::kRing) +
                       (static_cast<size_t>(n_max) + 1) * 4;
-  auto run = [&](auto attn, auto combine, auto weigh, int elem) -> int {
-    if (smem > 48 * 1024) {
-      if (cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess ||
-          cudaFuncSetAttribute(weigh, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-        return VLM_ERR_CUDA;
-    }
+  auto run = [&](auto attn, auto combine, auto weigh, int elem, bool ready) -> int {
+    if (!ready) return VLM_ERR_CUDA;
     for (int first = 0; first < c0.n_seqs; first += kMaxSeqs) {
       a.c = c0;
       a.c.n_seqs = std::min(kMaxSeqs, c0.n_seqs - first);
@@ -719,15 +857,18 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
     return VLM_OK;
   };
   launch_begin(KC_KV4_ATTN, s);
-  int rc;
-  if (dtype == VLM_DTYPE_F16)
-    rc = head_dim == 128 ? run(kv4_attn_kernel<__half, 128>, kv4_combine_kernel<__half, 128>, kv4_weights_kernel<__half, 128>, 2)
-                         : run(kv4_attn_kernel<__half, 64>, kv4_combine_kernel<__half, 64>, kv4_weights_kernel<__half, 64>, 2);
-  else
-    rc = head_dim == 128 ? run(kv4_attn_kernel<__nv_bfloat16, 128>, kv4_combine_kernel<__nv_bfloat16, 128>,
-                               kv4_weights_kernel<__nv_bfloat16, 128>, 2)
-                         : run(kv4_attn_kernel<__nv_bfloat16, 64>, kv4_combine_kernel<__nv_bfloat16, 64>,
-                               kv4_weights_kernel<__nv_bfloat16, 64>, 2);
+  auto pick = [&](auto type, auto dim, auto nt) {
+    using T = decltype(type);
+    constexpr int D = decltype(dim)::value, NT = decltype(nt)::value;
+    return run(kv4_attn_kernel<T, D, NT>, kv4_combine_kernel<T, D>, kv4_weights_kernel<T, D, NT>, 2, smem_ready<T, D, NT>());
+  };
+  auto by_rows = [&](auto type, auto dim) {
+    return one ? pick(type, dim, std::integral_constant<int, 1>()) : pick(type, dim, std::integral_constant<int, 2>());
+  };
+  auto by_dim = [&](auto type) {
+    return head_dim == 128 ? by_rows(type, std::integral_constant<int, 128>()) : by_rows(type, std::integral_constant<int, 64>());
+  };
+  const int rc = dtype == VLM_DTYPE_F16 ? by_dim(__half()) : by_dim(__nv_bfloat16());
   launch_end(KC_KV4_ATTN, s);
   note_extra_launches(((c0.n_seqs + kMaxSeqs - 1) / kMaxSeqs) * (weights != nullptr ? 3 : 2) - 1);
   return rc;

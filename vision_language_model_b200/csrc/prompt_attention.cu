@@ -419,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* xmax = reinterpret_cast<float*>(smem + C::kXch) + t * 4 * kRows;
     float* xsum = reinterpret_cast<float*>(smem + C::kXch) + 8 * kRows + t * 2 * kRows;
     const uint64_t sl2x2 = pair_f32(args.sl2);
+    const float grow_by = fminf(kRescaleThreshold / args.sl2, 1e38f);  // in the logits' own units, as the maximum is
     const int row_tok = r / args.group, row_head = r - row_tok * args.group;
     const bool wide = ((reinterpret_cast<uintptr_t>(args.out) | (args.out_stride * 2)) & 31) == 0;
     uint32_t sc = 0, oc = 0, vc_item = 0, live_items = 0;
@@ -471,18 +472,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < HK; ++c)
             if (c >= nvalid) u[c] = __float_as_uint(-INFINITY);
         }
-        const float m_own = row_max<true>(u) * args.sl2;
+        const float m_own = row_max<true>(u);
         xmax[((j & 1) * 2 + hf) * kRows + r] = m_own;
         bar_sync(pair_id, 64);
         const float m_cand = fmaxf(m_own, xmax[((j & 1) * 2 + (hf ^ 1)) * kRows + r]);
-        const bool grow = m_cand > m + kRescaleThreshold;
+        const bool grow = m_cand > m + grow_by;
         const float m_new = grow ? m_cand : m;
-        const float corr = grow ? ex2(m - m_new) : 1.0f;
+        const float corr = grow ? ex2((m - m_new) * args.sl2) : 1.0f;
         const bool any_grow = __any_sync(0xffffffffu, grow);
         m = m_new;
         const float ref = m == -INFINITY ? 0.0f : m;
         uint32_t pk[HK / 2];
-        const float sum = masked ? row_exp<false, kHalf>(u, sl2x2, ref, pk) : row_exp<true, kHalf>(u, sl2x2, ref, pk);
+        // Logits of ordinary size: 2^(s sl2 - m sl2) in one operation; the rounding of
+        // m sl2 scales the row's weights by up to 2^(2^-13) alike. Masked tiles and large
+        // logits: subtracted before they are scaled, and no polynomial.
+        const bool plain = !masked && !__any_sync(0xffffffffu, fabsf(ref * args.sl2) > 4096.0f);
+        const float sum = plain ? row_exp<true, kHalf>(u, sl2x2, ref * args.sl2, pk)
+                                : row_exp<false, kHalf, true>(u, sl2x2, ref, pk);
         l = l * corr + sum;
         if (!(m_own < INFINITY)) l = NAN;  // a NaN or infinite logit: exp2_poly would swallow it
         if (j > 0) {

@@ -34,6 +34,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -118,16 +123,20 @@ __device__ __forceinline__ float exp2_poly(float x) {
 
 // p_c = 2^(s_c * sl2 - m) for the thread's N scores of the row, packed as pairs (bf16,
 // or fp16 with kHalf) into pk; returns sum_c p_c (fp32, before rounding). The elements are independent.
+// kRaw: m is in the scores' own units and p_c = 2^((s_c - m) * sl2), one more
+// operation per pair, for scores of any size: a product rounded before it is
+// subtracted would be off by 2^-24 of itself, which counts from some 10^8 on.
 // kPoly: let exp2_poly take one pair in kPolyPairEvery (never on a tile with
 // masked keys, whose weights must be exactly 0).
-template <bool kPoly, bool kHalf = false, int N>
+template <bool kPoly, bool kHalf = false, bool kRaw = false, int N>
 __device__ __forceinline__ float row_exp(const uint32_t (&u)[N], uint64_t sl2x2, float m, uint32_t (&pk)[N / 2]) {
   const uint64_t negm2 = pair_f32(-m);
   uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int c = 0; c < N; c += 2) {
     float x0, x1, p0, p1;
-    unpack2(fma2(pack2(u[c], u[c + 1]), sl2x2, negm2), x0, x1);
+    unpack2(kRaw ? mul2(add2(pack2(u[c], u[c + 1]), negm2), sl2x2) : fma2(pack2(u[c], u[c + 1]), sl2x2, negm2), x0,
+            x1);
     if (kPoly && kPolyPairEvery > 0 && (c >> 1) % (kPolyPairEvery > 0 ? kPolyPairEvery : 1) == kPolyPairEvery - 1) {
       p0 = exp2_poly(x0);
       p1 = exp2_poly(x1);
