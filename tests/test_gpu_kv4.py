@@ -262,3 +262,46 @@ def test_pages_and_lengths_outside_the_cache_are_reported_and_touch_nothing():
         vlm.kv4_read(gp, U.cuda_int(t), K_SG, V_SG, U.cuda_int(cu), 3, start=U.cuda_int(n), status=status)
         assert vlm.status_sync(status) == vlm.ERR_BAD_PAGE
     assert torch.equal(gp.cpu(), torch.from_numpy(pages))
+
+
+@pytest.mark.parametrize("n_pages", [300, 262144, 262145])
+def test_eviction_checks_pages_of_small_and_large_pools(n_pages):
+    # the check's bit sets lie in shared memory up to 262,144 pages, in the workspace above
+    lens, budget = [200, 130], 64
+    pages = torch.zeros((n_pages, 1, T.page_bytes(64)), dtype=torch.uint8, device="cuda")
+    table = np.array([[0, n_pages - 1, 5, 7], [3, 4, 6, -1]], np.int32)
+    pages[torch.from_numpy(table.reshape(-1)[:7]).long().cuda()] = torch.randint(
+        0, 100, (7, 1, T.page_bytes(64)), dtype=torch.uint8, device="cuda")
+    w = torch.rand((2, 1, 256)).cuda()
+    for to, rc in (([[n_pages - 2], [8]], vlm.OK), ([[8], [n_pages - 1]], vlm.ERR_BAD_PAGE),
+                   ([[n_pages - 2], [n_pages - 2]], vlm.ERR_BAD_PAGE), ([[n_pages], [8]], vlm.ERR_BAD_PAGE)):
+        pool = pages.clone()
+        status = vlm.new_status()
+        new, kept, _ = vlm.kv4_evict(pool, U.cuda_int(table), U.cuda_int(lens), w, U.cuda_int(to), budget, recent=10,
+                                     status=status)
+        assert vlm.status_sync(status) == rc
+        if rc != vlm.OK:
+            assert torch.equal(pool, pages)
+            continue
+        for s in range(2):
+            ids = T.keep(w[s, 0].cpu().numpy(), lens[s], budget, 0, 10)
+            assert np.array_equal(kept[s, 0].cpu().numpy(), ids)
+            src = np.stack([pages[table[s, j // 64], 0, (j % 64) * 32:(j % 64 + 1) * 32].cpu().numpy() for j in ids])
+            assert np.array_equal(pool[to[s][0], 0, :2048].cpu().numpy().reshape(64, 32), src)
+
+
+def test_eviction_of_a_long_context():
+    # more places than a thread keeps in registers, and every 16-bit half of the counts in use
+    n, budget = 70_001, 33_000
+    pages, table, left = U.random_pool(31, [n], 1, 64, spare=-(-budget // PAGE))
+    rng = np.random.default_rng(6)
+    w = np.float32(rng.random((1, 1, table.shape[1] * PAGE)) ** 8)
+    w[w < 1e-4] = 0
+    status = vlm.new_status()
+    new, kept, gw = vlm.kv4_evict(guarded_copy(torch.from_numpy(pages)), U.cuda_int(table), U.cuda_int([n]),
+                                  guarded_copy(torch.from_numpy(w)), U.cuda_int(left[None, :-(-budget // PAGE)]), budget,
+                                  sinks=3, recent=500, status=status)
+    _ok(status)
+    ids = T.keep(w[0, 0], n, budget, 3, 500)
+    assert np.array_equal(kept[0, 0].cpu().numpy(), ids)
+    assert np.array_equal(gw[0, 0, :budget].cpu().numpy(), w[0, 0, ids])

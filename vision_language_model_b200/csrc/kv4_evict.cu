@@ -5,17 +5,24 @@
 // bit, with their weights.
 //
 // kv4_select_kernel, one CTA per (sequence, key head): the weight of the last
-//   place that still fits is found by a radix select over the weights' bits
-//   (four passes of eight bits, a histogram in shared memory each), then one
-//   ordered pass writes the kept places. The weights are 4 bytes per place and
-//   are read five times, from L2 after the first.
+//   place that still fits is found by a radix select over the weights' bits (11,
+//   11 and 10), then one ordered pass writes the kept places. Up to 16,384
+//   places the weights stay in registers and are read once. Softmax weights
+//   share a few exponents, and what bounds the count of a digit is atomics on
+//   one address: hence digits that reach into the mantissa, four copies of the
+//   histogram, and places of weight 0 (many, as a rule) counted by ballots.
+//   With digits of 8 bits, whose first is all exponent, and one copy: 25 us for
+//   64 (sequence, head) pairs of 16,384 places, now 11 us.
 // kv4_move_kernel, one CTA per destination page of a head: 16-byte copies of
-//   the kept rows, 9/8 byte per column in and out: bound by HBM.
-// Fresh pages have to be fresh: one more CTA per sequence marks its source and
-// destination pages in two bit sets of the pool and compares them; on a
-// destination page that is also a source page, or is named twice, no page is
-// written and the status word says so. Marking before comparing lets the CTAs
-// run in any order: of two that meet, the later one sees the earlier's mark.
+//   the kept rows, 9/8 byte per column in and out: bound by HBM, whose 64-byte
+//   pieces a row's two 8-byte scale groups use by an eighth.
+// Fresh pages have to be fresh: one more CTA marks all source and destination
+// pages in two bit sets of the pool and compares them; on a destination page
+// that is also a source page, or is named twice, no page is written and the
+// status word says so. The bit sets lie in shared memory for pools of up to
+// 262,144 pages; for larger ones in the workspace, cleared first, with one CTA
+// per sequence: marking before comparing lets the CTAs run in any order, of two
+// that meet the later one sees the earlier's mark.
 #include <algorithm>
 
 #include "kv4.cuh"
@@ -26,8 +33,13 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kPer = 4;  // places per thread and step of the ordered pass
+constexpr int kPer = 4;       // consecutive places per thread and step
+constexpr int kCopies = 4;    // of a digit's histogram, side by side
+constexpr int kDigits = 2048;
+constexpr int kCached = 4;    // steps whose weights a thread keeps in registers
 constexpr int kMoveThreads = 128;
+constexpr int64_t kSharedPages = 262144;  // pools up to here are marked in shared memory
+constexpr uint32_t kZeroKey = 0x80000000u;
 
 struct EvictArgs {
   Kv4 c;
@@ -38,7 +50,7 @@ struct EvictArgs {
   int32_t* to_lens;
   float* to_weights;  // [n_seqs, kv_heads, to_max_pages * 64]
   int32_t* kept;      // [n_seqs, kv_heads, budget]
-  uint32_t *src_bits, *dst_bits;
+  uint32_t *src_bits, *dst_bits;  // null: in shared memory
   int32_t* clash;
   int32_t* status;
 };
@@ -50,13 +62,65 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ void mark_pages(const EvictArgs& a, int s, int n, int n_new) {
+// Entry e of sequence s: the source pages, then the destination pages.
+__device__ __forceinline__ int32_t page_entry(const EvictArgs& a, int s, int e, int src, bool& is_dst) {
+  is_dst = e >= src;
+  return is_dst ? __ldg(a.to_table + static_cast<int64_t>(s) * a.to_max_pages + e - src)
+                : __ldg(a.c.table + static_cast<int64_t>(s) * a.c.max_pages + e);
+}
+
+__device__ void mark_shared(const EvictArgs& a, uint32_t* bits) {
+  const int words = static_cast<int>((a.c.n_pages + 31) / 32);
+  uint32_t* dst_bits = bits + words;
+  for (int i = threadIdx.x; i < 2 * words; i += kSelThreads) bits[i] = 0;
+  __syncthreads();
+  // a warp takes 32 entries of a sequence at a time, so that many are looked up at once
+  __shared__ int lens[kSelThreads];
+  bool bad = false;
+  const int chunks = (a.c.max_pages + a.to_max_pages + 31) / 32;
+  for (int s0 = 0; s0 < a.c.n_seqs; s0 += kSelThreads) {
+    const int count = min(kSelThreads, a.c.n_seqs - s0);
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < count) {
+      const int n = kv4_len(a.c, s0 + threadIdx.x, a.status);
+      lens[threadIdx.x] = n;
+      a.to_lens[s0 + threadIdx.x] = min(n, a.budget);
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int task = threadIdx.x >> 5; task < count * chunks; task += kSelWarps) {
+      const int s = task / chunks, e = (task - s * chunks) * 32 + (threadIdx.x & 31);
+      const int n = lens[s], n_new = min(n, a.budget);
+      const int src = (n + kKv4Page - 1) / kKv4Page, dst = (n_new + kKv4Page - 1) / kKv4Page;
+      if (e >= src + dst) continue;
+      bool is_dst;
+      const int32_t p = page_entry(a, s0 + s, e, src, is_dst);
+      if (static_cast<uint32_t>(p) >= static_cast<uint64_t>(a.c.n_pages)) {
+        bad = true;
+        continue;
+      }
+      const uint32_t bit = 1u << (p & 31);
+      const uint32_t old = atomicOr((is_dst ? dst_bits : bits) + (p >> 5), bit);
+      if (is_dst && (old & bit) != 0) bad = true;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < words; i += kSelThreads) bad |= (bits[i] & dst_bits[i]) != 0;
+  const int any = __syncthreads_or(bad);
+  if (threadIdx.x == 0) {
+    *a.clash = any;
+    if (any) set_status(a.status, VLM_ERR_BAD_PAGE);
+  }
+}
+
+__device__ void mark_global(const EvictArgs& a, int s) {
+  const int n = kv4_len(a.c, s, threadIdx.x == 0 ? a.status : nullptr), n_new = min(n, a.budget);
+  if (threadIdx.x == 0) a.to_lens[s] = n_new;
   const int src = (n + kKv4Page - 1) / kKv4Page, dst = (n_new + kKv4Page - 1) / kKv4Page;
   bool bad = false;
   for (int e = threadIdx.x; e < src + dst; e += kSelThreads) {
-    const bool is_dst = e >= src;
-    const int32_t p = is_dst ? __ldg(a.to_table + static_cast<int64_t>(s) * a.to_max_pages + e - src)
-                             : __ldg(a.c.table + static_cast<int64_t>(s) * a.c.max_pages + e);
+    bool is_dst;
+    const int32_t p = page_entry(a, s, e, src, is_dst);
     if (static_cast<uint32_t>(p) >= static_cast<uint64_t>(a.c.n_pages)) {
       bad = true;
       continue;
@@ -73,20 +137,45 @@ __device__ void mark_pages(const EvictArgs& a, int s, int n, int n_new) {
   }
 }
 
+// Inclusive sum over the CTA's threads in order; `total` their sum. Two barriers.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, uint32_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) warp_sum[warp] = v;
+  __syncthreads();
+  uint32_t w = warp_sum[lane];  // one per warp: kSelWarps is 32
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += u;
+  }
+  total = __shfl_sync(0xffffffffu, w, 31);
+  const uint32_t before = warp == 0 ? 0 : __shfl_sync(0xffffffffu, w, warp - 1);
+  __syncthreads();
+  return v + before;
+}
+
 __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const EvictArgs a) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t found[2];  // the digit, and how many are still wanted below it
+  extern __shared__ __align__(16) uint32_t dyn[];  // the histogram's copies, or the pool's two bit sets
   __shared__ uint32_t warp_sum[kSelWarps];
+  __shared__ uint32_t found[2];  // the digit, and how many of its places are still wanted
+  static_assert(kSelWarps == 32, "block_scan");
   griddep_wait();
   griddep_launch_dependents();
   const int s = blockIdx.y, h = blockIdx.x, tid = threadIdx.x;
-  const int n = kv4_len(a.c, s, h == 0 && tid == 0 ? a.status : nullptr);
-  const int n_new = min(n, a.budget);
   if (h == a.c.kv_heads) {
-    mark_pages(a, s, n, n_new);
-    if (tid == 0) a.to_lens[s] = n_new;
+    if (a.src_bits != nullptr)
+      mark_global(a, s);
+    else if (s == 0)
+      mark_shared(a, dyn);
     return;
   }
+  const int n = kv4_len(a.c, s, nullptr);
+  const int n_new = min(n, a.budget);
   const int64_t unit = static_cast<int64_t>(s) * a.c.kv_heads + h;
   const float* w = a.weights + unit * a.c.max_pages * kKv4Page;
   float* to_w = a.to_weights + unit * a.to_max_pages * kKv4Page;
@@ -102,92 +191,114 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const EvictArgs
   }
   const int lo = a.sinks, hi = n - a.recent;  // the places that compete; more of them than are wanted
   uint32_t want = static_cast<uint32_t>(a.budget - a.sinks - a.recent);
-  uint32_t prefix = 0;  // the digits found so far
-  if (want > 0) {
-#pragma unroll 1
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-#pragma unroll 4
-      for (int j = lo + tid; j < hi; j += kSelThreads) {
-        const uint32_t k = key_of(__ldg(w + j));
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+  uint32_t least = 0xFFFFFFFFu;  // the smallest kept key; nothing wanted: above every key
+  constexpr int kStep = kSelThreads * kPer;
+  const int steps = (n + kStep - 1) / kStep;
+  // a thread's places are kPer consecutive ones of every step
+  auto load = [&](int step, float (&x)[kPer]) {
+    const int j = step * kStep + tid * kPer;
+    if (j + kPer <= n) {  // rows of weights are whole pages: 16-byte aligned as long as the array is
+      if ((reinterpret_cast<uintptr_t>(w) & 15) == 0) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(w + j));
+        x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
+        return;
       }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = j + i < n ? __ldg(w + j + i) : 0.0f;
+  };
+  // keys, and which places compete (bit kPer step + i), of the first steps
+  uint32_t cache[kCached][kPer], competes = 0;
+  auto range = [&](int step) {
+    const int j = step * kStep + tid * kPer;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) m |= (j + i >= lo && j + i < hi ? 1u : 0u) << i;
+    return m;
+  };
+  {
+    float x[kCached][kPer];
+#pragma unroll
+    for (int c = 0; c < kCached; ++c)
+      if (c < steps) load(c, x[c]);
+#pragma unroll
+    for (int c = 0; c < kCached; ++c) {
+      if (c < steps) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) cache[c][i] = key_of(x[c][i]);
+        competes |= range(c) << (kPer * c);
+      }
+    }
+  }
+  if (want > 0) {
+    uint32_t prefix = 0;  // the digits found so far
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t digit = pass == 2 ? 1023u : 2047u;
+      const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
+      for (int i = tid; i < kCopies * kDigits / 4; i += kSelThreads) reinterpret_cast<uint4*>(dyn)[i] = make_uint4(0, 0, 0, 0);
       __syncthreads();
-      // the largest digit with at least `want` keys at or above it
-      if (tid < 32) {
-        uint32_t cnt[8], sum = 0;
+      uint32_t* mine = dyn + tid % kCopies;  // neighbouring lanes count in different copies, in different banks
+      uint32_t zeros = 0;
+      const bool with_zeros = (kZeroKey & mask) == prefix;
+      auto count = [&](uint32_t in, const uint32_t (&k)[kPer]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          cnt[i] = hist[255 - (tid * 8 + i)];
-          sum += cnt[i];
+        for (int i = 0; i < kPer; ++i) {
+          const bool counts = ((in >> i) & 1) && (k[i] & mask) == prefix;
+          if (with_zeros) zeros += __popc(__ballot_sync(0xffffffffu, counts && k[i] == kZeroKey));
+          if (counts && k[i] != kZeroKey) atomicAdd(mine + ((k[i] >> shift) & digit) * kCopies, 1u);
         }
-        uint32_t inc = sum;
+      };
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
-          if (tid >= o) inc += v;
-        }
-        uint32_t above = inc - sum;
-        if (above < want && want <= inc) {
+      for (int c = 0; c < kCached; ++c)
+        if (c < steps) count(competes >> (kPer * c), cache[c]);
+      for (int c = kCached; c < steps; ++c) {
+        float x[kPer];
+        uint32_t k[kPer];
+        load(c, x);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (above < want && want <= above + cnt[i]) {
-              found[0] = 255 - (tid * 8 + i);
-              found[1] = want - above;
-            }
-            above += cnt[i];
-          }
-        }
+        for (int i = 0; i < kPer; ++i) k[i] = key_of(x[i]);
+        count(range(c), k);
+      }
+      if ((tid & 31) == 0 && zeros > 0) atomicAdd(mine + ((kZeroKey >> shift) & digit) * kCopies, zeros);
+      __syncthreads();
+      // digits from the top, two per thread: the largest with `want` keys at or above it
+      uint32_t cnt[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4 c = reinterpret_cast<const uint4*>(dyn)[kDigits - 1 - (2 * tid + i)];
+        cnt[i] = c.x + c.y + c.z + c.w;
+      }
+      uint32_t total;
+      const uint32_t inc = block_scan(cnt[0] + cnt[1], warp_sum, total);
+      const uint32_t above = inc - cnt[0] - cnt[1];
+      if (above < want && want <= inc) {
+        const int second = want > above + cnt[0];
+        found[0] = kDigits - 1 - (2 * tid + second);
+        found[1] = want - above - (second ? cnt[0] : 0);
       }
       __syncthreads();
       prefix |= found[0] << shift;
       want = found[1];
-      __syncthreads();
     }
+    least = prefix;
   }
-  // `prefix` is the smallest kept key, `want` of its places are kept, the first ones.
-  // With nothing wanted no key counts (want 0 and nothing above the top key).
-  const uint32_t least = a.budget > a.sinks + a.recent ? prefix : 0xFFFFFFFFu;
-  uint32_t base = 0;  // places above in the low half's count, equal ones in `eq`
-  uint32_t base_eq = 0;
-  for (int first = 0; first < n; first += kSelThreads * kPer) {
-    const int j0 = first + tid * kPer;
-    float x[kPer];
+  // every key above `least`, and the first `want` places of it
+  uint32_t base = 0, base_eq = 0;
+  auto emit = [&](int step, uint32_t in, const uint32_t (&k)[kPer]) {
+    const int j0 = step * kStep + tid * kPer;
     uint32_t take = 0, equal = 0;  // bit masks over the thread's places
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int j = j0 + i;
-      x[i] = j < n ? __ldg(w + j) : 0.0f;
-      if (j < n) {
-        if (j < lo || j >= hi) {
-          take |= 1u << i;
-        } else {
-          const uint32_t k = key_of(x[i]);
-          if (k > least) take |= 1u << i;
-          if (k == least) equal |= 1u << i;
-        }
-      }
+      const bool competing = (in >> i) & 1;
+      if (competing ? k[i] > least : j0 + i < n) take |= 1u << i;
+      if (competing && k[i] == least) equal |= 1u << i;
     }
     // both counts in one word: at most 4,096 each per step
     const uint32_t mine = __popc(take) | (__popc(equal) << 16);
-    uint32_t inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
-      if ((tid & 31) >= o) inc += v;
-    }
-    if ((tid & 31) == 31) warp_sum[tid >> 5] = inc;
-    __syncthreads();
-    uint32_t before = 0, total = 0;
-#pragma unroll
-    for (int i = 0; i < kSelWarps; ++i) {
-      const uint32_t v = warp_sum[i];
-      if (i < (tid >> 5)) before += v;
-      total += v;
-    }
-    const uint32_t excl = before + inc - mine;
+    uint32_t total;
+    const uint32_t excl = block_scan(mine, warp_sum, total) - mine;
     uint32_t taken = base + (excl & 0xFFFFu), eq = base_eq + (excl >> 16);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -196,7 +307,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const EvictArgs
         const uint32_t at = taken + min(eq, want);
         if (at < static_cast<uint32_t>(n_new)) {
           kept[at] = j0 + i;
-          to_w[at] = x[i];
+          to_w[at] = __ldg(w + j0 + i);
         }
       }
       taken += (take >> i) & 1;
@@ -204,7 +315,17 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const EvictArgs
     }
     base += total & 0xFFFFu;
     base_eq += total >> 16;
-    __syncthreads();
+  };
+#pragma unroll
+  for (int c = 0; c < kCached; ++c)
+    if (c < steps) emit(c, competes >> (kPer * c), cache[c]);
+  for (int c = kCached; c < steps; ++c) {
+    float x[kPer];
+    uint32_t k[kPer];
+    load(c, x);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) k[i] = key_of(x[i]);
+    emit(c, range(c), k);
   }
 }
 
@@ -252,24 +373,40 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 }  // namespace
 
 size_t kv4_evict_workspace(int64_t n_pages, int n_seqs, int kv_heads, int budget) {
-  return 256 + 2 * up(static_cast<size_t>((n_pages + 31) / 32) * 4) +
+  const size_t bits = n_pages <= kSharedPages ? 0 : 2 * up(static_cast<size_t>((n_pages + 31) / 32) * 4);
+  return 256 + bits +
          up(static_cast<size_t>(n_seqs) * kv_heads * budget * 4);
 }
 
 int launch_kv4_evict(const Kv4& c, int head_dim, const float* weights, int budget, int sinks, int recent,
                      const int32_t* to_table, int to_max_pages, int32_t* to_lens, float* to_weights, int32_t* kept,
                      void* ws, int32_t* status, cudaStream_t s) {
-  const size_t bits = up(static_cast<size_t>((c.n_pages + 31) / 32) * 4);
+  const bool shared = c.n_pages <= kSharedPages;
+  const size_t bits = shared ? 0 : up(static_cast<size_t>((c.n_pages + 31) / 32) * 4);
   uint8_t* w = static_cast<uint8_t*>(ws);
   EvictArgs a{c, weights, budget, sinks, recent, to_table, to_max_pages, to_lens, to_weights, kept, nullptr, nullptr,
               nullptr, status};
   a.clash = reinterpret_cast<int32_t*>(w);
-  a.src_bits = reinterpret_cast<uint32_t*>(w + 256);
-  a.dst_bits = reinterpret_cast<uint32_t*>(w + 256 + bits);
   if (kept == nullptr) a.kept = reinterpret_cast<int32_t*>(w + 256 + 2 * bits);
-  if (cudaMemsetAsync(w, 0, 256 + 2 * bits, s) != cudaSuccess) return VLM_ERR_CUDA;
+  size_t smem = kCopies * kDigits * 4;
+  if (shared) {
+    smem = std::max(smem, static_cast<size_t>((c.n_pages + 31) / 32) * 8);
+  } else {
+    a.src_bits = reinterpret_cast<uint32_t*>(w + 256);
+    a.dst_bits = reinterpret_cast<uint32_t*>(w + 256 + bits);
+    if (cudaMemsetAsync(w, 0, 256 + 2 * bits, s) != cudaSuccess) return VLM_ERR_CUDA;
+  }
+  static bool ready[64] = {};  // 64 KB of shared memory, once per device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return VLM_ERR_CUDA;
+  if (dev >= 64 || !ready[dev]) {
+    if (cudaFuncSetAttribute(kv4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSharedPages / 32 * 8)) != cudaSuccess)
+      return VLM_ERR_CUDA;
+    if (dev < 64) ready[dev] = true;
+  }
   launch_begin(KC_KV4_EVICT, s);
-  cudaError_t e = launch_pdl(kv4_select_kernel, dim3(c.kv_heads + 1, c.n_seqs), dim3(kSelThreads), 0, s, a);
+  cudaError_t e = launch_pdl(kv4_select_kernel, dim3(c.kv_heads + 1, c.n_seqs), dim3(kSelThreads), smem, s, a);
   const dim3 grid((budget + kKv4Page - 1) / kKv4Page, c.kv_heads, c.n_seqs);
   if (e == cudaSuccess)
     e = head_dim == 128 ? launch_pdl(kv4_move_kernel<128>, grid, dim3(kMoveThreads), 0, s, a)

@@ -737,45 +737,83 @@ def _dtype16(dtype: torch.dtype) -> int:
     return code
 
 
-def _rows16(t: torch.Tensor, name: str, like: torch.Tensor) -> tuple:
-    """(pointer, elements between tokens) of 16-bit [tokens, heads, head_dim] rows, heads contiguous."""
-    if t.dim() != 3:
+def _rows16(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int) -> tuple:
+    """(pointer, elements between tokens) of 16-bit [tokens, heads, head_dim] rows, heads contiguous,
+    on CUDA device number dev."""
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if t.device != like.device or not t.is_cuda:
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the CUDA device of the other operands")
-    n, heads, dim = t.shape
-    if n and heads and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+    n, heads, dim = shape
+    s0, s1, s2 = t.stride()
+    if n and heads and (s2 != 1 or (s1 != dim and heads > 1)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), t.stride(0) if n > 1 else heads * dim
+    return t.data_ptr(), s0 if n > 1 else heads * dim
 
 
-def _int32_dev(t: torch.Tensor | None, name: str, shape: tuple, dev: torch.device) -> int | None:
+def _plain(t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple, dev: int) -> int | None:
+    """Pointer of a contiguous tensor of this type and shape on CUDA device number dev."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
-    return _dev(t, name)
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the CUDA device of the other operands")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-class _on:
-    """Makes `dev` the current device for a call whose tensors live there."""
+def _cuda_of(t: torch.Tensor, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
 
-    def __init__(self, dev: torch.device):
-        self.dev, self.old = dev.index, None
+
+class _On:
+    """Makes CUDA device number dev the current one for a call whose tensors live there."""
+
+    def __init__(self, dev: int):
+        self.dev, self.old = dev, torch.cuda.current_device()
 
     def __enter__(self):
-        cur = torch.cuda.current_device()
-        if self.dev is not None and cur != self.dev:
-            self.old = cur
-            torch.cuda.set_device(self.dev)
+        torch.cuda.set_device(self.dev)
 
     def __exit__(self, *exc):
-        if self.old is not None:
-            torch.cuda.set_device(self.old)
+        torch.cuda.set_device(self.old)
+
+
+class _Here:
+    """The device is the current one already."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_HERE = _Here()
+
+
+def _on(dev: int):
+    return _HERE if torch._C._cuda_getDevice() == dev else _On(dev)
+
+
+def _stream_on(dev: int, stream) -> int:
+    """The given stream, else the current one of CUDA device number dev."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _status_ptr(status: torch.Tensor | None, dev: int) -> int:
+    """The caller's status word; without one a word of this call's own, which nobody reads."""
+    if status is None:
+        status = new_status(torch.device("cuda", dev))
+    return _plain(status, "status", torch.int32, (1,), dev)
 
 
 def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_lens, kv_lens=None,
@@ -786,32 +824,34 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_lens, 
     stride between tokens (column blocks of one projection's output). q_lens, kv_lens: host lists;
     kv_lens None: the same. The last query of a sequence sees every key. scale None:
     1 / sqrt(head_dim). Returns out [sum(q_lens), heads, head_dim]."""
-    q_lens = [int(n) for n in q_lens]
-    kv_lens = q_lens if kv_lens is None else [int(n) for n in kv_lens]
     n = len(q_lens)
+    if kv_lens is None:
+        kv_lens = q_lens
     if len(kv_lens) != n:
         raise ValueError("q_lens and kv_lens must list the same sequences")
-    dt = _dtype16(q.dtype)
-    qp, qs = _rows16(q, "q", q)
-    kp, ks = _rows16(k, "k", q)
-    vp, vs = _rows16(v, "v", q)
+    dev, dtype = _cuda_of(q, "q"), q.dtype
+    dt = _dtype16(dtype)
+    qp, qs = _rows16(q, "q", dtype, dev)
+    kp, ks = _rows16(k, "k", dtype, dev)
+    vp, vs = _rows16(v, "v", dtype, dev)
     T, heads, dim = q.shape
-    if k.shape != v.shape or k.shape[2] != dim:
+    tk, kv_heads, kdim = k.shape
+    if k.shape != v.shape or kdim != dim:
         raise ValueError("k and v must have one shape and q's head_dim")
-    if sum(q_lens) != T or sum(kv_lens) != k.shape[0]:
-        raise ValueError(f"the lengths add up to {sum(q_lens)} and {sum(kv_lens)}, q has {T} rows and k {k.shape[0]}")
-    with _on(q.device):
+    if sum(q_lens) != T or sum(kv_lens) != tk:
+        raise ValueError(f"the lengths add up to {sum(q_lens)} and {sum(kv_lens)}, q has {T} rows and k {tk}")
+    with _on(dev):
         if out is None:
-            out = _empty((T, heads, dim), dtype=q.dtype, device=q.device)
-        elif tuple(out.shape) != (T, heads, dim):
-            raise ValueError("out must have q's shape")
-        op, os_ = _rows16(out, "out", q)
-        if status is None:
-            status = new_status(q.device)
+            out = _empty((T, heads, dim), dtype, q.device)
+            op, os_ = out.data_ptr(), heads * dim
+        else:
+            if out.shape != q.shape:
+                raise ValueError("out must have q's shape")
+            op, os_ = _rows16(out, "out", dtype, dev)
         arr = ctypes.c_int32 * max(1, n)
-        _check(lib().vlm_prompt_attention(dt, heads, k.shape[1], dim, arr(*q_lens), arr(*kv_lens), n, qp, qs, kp, ks,
-                                          vp, vs, float(dim ** -0.5 if scale is None else scale), op, os_,
-                                          _dev(status, "status"), _stream(stream)), "vlm_prompt_attention")
+        _check(lib().vlm_prompt_attention(dt, heads, kv_heads, dim, arr(*q_lens), arr(*kv_lens), n, qp, qs, kp, ks,
+                                          vp, vs, dim ** -0.5 if scale is None else scale, op, os_,
+                                          _status_ptr(status, dev), _stream_on(dev, stream)), "vlm_prompt_attention")
     return out
 
 
@@ -829,14 +869,20 @@ def kv4_pages(n_pages: int, kv_heads: int, head_dim: int, device="cuda") -> torc
 
 
 def _kv4(pages: torch.Tensor, table: torch.Tensor, k_sg: float, v_sg: float) -> tuple:
-    """(descriptor, table pointer, entries per row, sequences) of a cache and its page table."""
-    if pages.dtype != torch.uint8 or pages.dim() != 3 or pages.shape[2] not in (KV4_PAGE * 72, KV4_PAGE * 144):
+    """(descriptor, table pointer, entries per row, sequences, device, kv_heads, head_dim) of a cache and its page table."""
+    shape = pages.shape
+    if pages.dtype is not torch.uint8 or len(shape) != 3 or shape[2] not in (KV4_PAGE * 72, KV4_PAGE * 144):
         raise ValueError("pages must be uint8 [n_pages, kv_heads, page bytes] as kv4_pages makes them")
-    if table.dim() != 2:
+    if len(table.shape) != 2:
         raise ValueError("table must be int32 [n_seqs, max_pages]")
-    tp = _int32_dev(table, "table", tuple(table.shape), pages.device)
-    desc = Kv4CacheDesc(_dev(pages, "pages"), pages.shape[0], pages.shape[1], pages.shape[2] // 72, k_sg, v_sg)
-    return ctypes.byref(desc), tp, table.shape[1], table.shape[0]
+    dev = _cuda_of(pages, "pages")
+    n, width = table.shape
+    tp = _plain(table, "table", torch.int32, (n, width), dev)
+    dim = shape[2] // 72
+    if not pages.is_contiguous():
+        raise ValueError("pages must be contiguous")
+    desc = Kv4CacheDesc(pages.data_ptr(), shape[0], shape[1], dim, k_sg, v_sg)
+    return ctypes.byref(desc), tp, width, n, dev, shape[1], dim
 
 
 def kv4_append(pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
@@ -845,19 +891,18 @@ def kv4_append(pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor | No
     lens[s] on (vlm_kv4_append). table int32 [n_seqs, max_pages] and lens int32 [n_seqs] (None: 0) are
     device tensors, as is cu_new int32 [n_seqs + 1], the rows of each sequence (None: one row each).
     The global scales k_sg, v_sg are the cache's for good. lens is not advanced."""
-    desc, tp, width, n = _kv4(pages, table, k_sg, v_sg)
-    dev = pages.device
-    dt = _dtype16(k.dtype)
-    kp, ks = _rows16(k, "k", k)
-    vp, vs = _rows16(v, "v", k)
-    if k.device != dev or k.shape != v.shape or k.shape[1] != pages.shape[1] or k.shape[2] != pages.shape[2] // 72:
-        raise ValueError("k and v must be [n_new, kv_heads, head_dim] of the cache, on its device")
+    desc, tp, width, n, dev, kv_heads, dim = _kv4(pages, table, k_sg, v_sg)
+    dtype = k.dtype
+    dt = _dtype16(dtype)
+    kp, ks = _rows16(k, "k", dtype, dev)
+    vp, vs = _rows16(v, "v", dtype, dev)
+    n_new = k.shape[0]
+    if k.shape != v.shape or k.shape[1] != kv_heads or k.shape[2] != dim:
+        raise ValueError("k and v must be [n_new, kv_heads, head_dim] of the cache")
     with _on(dev):
-        if status is None:
-            status = new_status(dev)
-        _check(lib().vlm_kv4_append(desc, tp, width, n, _int32_dev(lens, "lens", (n,), dev),
-                                    _int32_dev(cu_new, "cu_new", (n + 1,), dev), k.shape[0], dt, kp, ks, vp, vs,
-                                    _dev(status, "status"), _stream(stream)), "vlm_kv4_append")
+        _check(lib().vlm_kv4_append(desc, tp, width, n, _plain(lens, "lens", torch.int32, (n,), dev),
+                                    _plain(cu_new, "cu_new", torch.int32, (n + 1,), dev), n_new, dt, kp, ks, vp, vs,
+                                    _status_ptr(status, dev), _stream_on(dev, stream)), "vlm_kv4_append")
 
 
 def kv4_read(pages: torch.Tensor, table: torch.Tensor, k_sg: float, v_sg: float, cu: torch.Tensor | None, n_rows: int,
@@ -865,27 +910,35 @@ def kv4_read(pages: torch.Tensor, table: torch.Tensor, k_sg: float, v_sg: float,
              stream=None) -> tuple:
     """Rows of the cache in 16 bits (vlm_kv4_read): k, v [n_rows, kv_heads, head_dim], the rows
     [cu[s], cu[s + 1]) from sequence s's places start[s] on (None: 0; cu None: one row each)."""
-    desc, tp, width, n = _kv4(pages, table, k_sg, v_sg)
-    dev = pages.device
-    shape = (int(n_rows), pages.shape[1], pages.shape[2] // 72)
+    desc, tp, width, n, dev, kv_heads, dim = _kv4(pages, table, k_sg, v_sg)
+    if k is not None:
+        dtype = k.dtype
+    dt = _dtype16(dtype)
+    shape = (n_rows, kv_heads, dim)
     with _on(dev):
-        k = _empty(shape, dtype=dtype, device=dev) if k is None else k
-        v = _empty(shape, dtype=dtype, device=dev) if v is None else v
-        dt = _dtype16(k.dtype)
-        if tuple(k.shape) != shape or tuple(v.shape) != shape or v.dtype != k.dtype or k.device != dev \
-                or v.device != dev:
-            raise ValueError(f"k and v must be {list(shape)} of one type, on the cache's device")
-        if status is None:
-            status = new_status(dev)
-        _check(lib().vlm_kv4_read(desc, tp, width, n, _int32_dev(start, "start", (n,), dev),
-                                  _int32_dev(cu, "cu", (n + 1,), dev), int(n_rows), dt, _dev(k, "k"), _dev(v, "v"),
-                                  _dev(status, "status"), _stream(stream)), "vlm_kv4_read")
+        if k is None:
+            k = _empty(shape, dtype, pages.device)
+        if v is None:
+            v = _empty(shape, dtype, pages.device)
+        _check(lib().vlm_kv4_read(desc, tp, width, n, _plain(start, "start", torch.int32, (n,), dev),
+                                  _plain(cu, "cu", torch.int32, (n + 1,), dev), n_rows, dt,
+                                  _plain(k, "k", dtype, shape, dev), _plain(v, "v", dtype, shape, dev),
+                                  _status_ptr(status, dev), _stream_on(dev, stream)), "vlm_kv4_read")
     return k, v
 
 
 def kv4_attention_workspace_size(n_seqs: int, heads: int, kv_heads: int, head_dim: int, q_len: int = 1) -> int:
     return int(lib().vlm_kv4_attention_workspace_size(int(n_seqs), int(heads), int(kv_heads), int(head_dim),
                                                       int(q_len)))
+
+
+def _workspace(ws: torch.Tensor | None, need, dev: int) -> tuple:
+    """(tensor, pointer, bytes) of the caller's uint8 workspace, or of a new one of need() bytes."""
+    if ws is None:
+        ws = _empty(max(256, need()), torch.uint8, torch.device("cuda", dev))
+    elif ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous uint8 on the CUDA device of the other operands")
+    return ws, ws.data_ptr(), ws.numel()
 
 
 def kv4_attention(pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, q: torch.Tensor, k_sg: float,
@@ -895,32 +948,25 @@ def kv4_attention(pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, 
     (vlm_kv4_attention). q [n_seqs * q_len, heads, head_dim] bf16 or fp16; lens: device int32 [n_seqs],
     the new tokens included. weights: fp32 [n_seqs, kv_heads, max_pages * 64], to which every place's
     softmax weight is added, summed over the new tokens and the key head's query heads."""
-    desc, tp, width, n = _kv4(pages, table, k_sg, v_sg)
-    dev = pages.device
-    dt = _dtype16(q.dtype)
-    qp, qs = _rows16(q, "q", q)
-    T, heads, dim = q.shape
-    if q.device != dev or n == 0 or T == 0 or T % n != 0 or dim != pages.shape[2] // 72:
-        raise ValueError("q must be [n_seqs * q_len, heads, head_dim] of the cache, on its device")
-    kv_heads, m = pages.shape[1], T // n
-    if weights is not None and (weights.dtype != torch.float32 or weights.device != dev
-                                or tuple(weights.shape) != (n, kv_heads, width * KV4_PAGE)):
-        raise ValueError("weights must be fp32 [n_seqs, kv_heads, max_pages * 64]")
+    desc, tp, width, n, dev, kv_heads, dim = _kv4(pages, table, k_sg, v_sg)
+    dtype = q.dtype
+    dt = _dtype16(dtype)
+    qp, qs = _rows16(q, "q", dtype, dev)
+    T, heads, qdim = q.shape
+    if n == 0 or T == 0 or T % n != 0 or qdim != dim:
+        raise ValueError("q must be [n_seqs * q_len, heads, head_dim] of the cache")
+    m = T // n
+    wp = _plain(weights, "weights", torch.float32, (n, kv_heads, width * KV4_PAGE), dev)
     L = lib()
     with _on(dev):
         if out is None:
-            out = _empty((T, heads, dim), dtype=q.dtype, device=dev)
-        elif tuple(out.shape) != (T, heads, dim) or out.dtype != q.dtype or out.device != dev:
-            raise ValueError("out must have q's shape, type and device")
-        if workspace is None:
-            workspace = _empty(max(256, L.vlm_kv4_attention_workspace_size(n, heads, kv_heads, dim, m)),
-                               dtype=torch.uint8, device=dev)
-        if status is None:
-            status = new_status(dev)
-        _check(L.vlm_kv4_attention(desc, tp, width, n, _int32_dev(lens, "lens", (n,), dev), dt, heads, m, qp, qs,
-                                   float(dim ** -0.5 if scale is None else scale), _dev(out, "out"),
-                                   _dev(weights, "weights"), _dev(workspace, "workspace"), workspace.numel(),
-                                   _dev(status, "status"), _stream(stream)), "vlm_kv4_attention")
+            out = _empty((T, heads, dim), dtype, pages.device)
+        ws, ws_ptr, ws_bytes = _workspace(workspace, lambda: L.vlm_kv4_attention_workspace_size(n, heads, kv_heads, dim, m),
+                                          dev)
+        _check(L.vlm_kv4_attention(desc, tp, width, n, _plain(lens, "lens", torch.int32, (n,), dev), dt, heads, m, qp,
+                                   qs, dim ** -0.5 if scale is None else scale,
+                                   _plain(out, "out", dtype, (T, heads, dim), dev), wp, ws_ptr, ws_bytes,
+                                   _status_ptr(status, dev), _stream_on(dev, stream)), "vlm_kv4_attention")
     return out
 
 
@@ -935,36 +981,29 @@ def kv4_evict(pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, weig
     and those with the largest summed weights -- and moves them to the fresh pages of to_table int32
     [n_seqs, to_max_pages] (vlm_kv4_evict). Returns (to_lens int32 [n_seqs], kept int32
     [n_seqs, kv_heads, budget], to_weights fp32 [n_seqs, kv_heads, to_max_pages * 64])."""
-    desc, tp, width, n = _kv4(pages, table, 1.0, 1.0)
-    dev, kv_heads, budget = pages.device, pages.shape[1], int(budget)
-    if weights.dtype != torch.float32 or weights.device != dev \
-            or tuple(weights.shape) != (n, kv_heads, width * KV4_PAGE):
-        raise ValueError("weights must be fp32 [n_seqs, kv_heads, max_pages * 64]")
-    if to_table.dim() != 2 or budget < 1:
+    desc, tp, width, n, dev, kv_heads, _ = _kv4(pages, table, 1.0, 1.0)
+    if len(to_table.shape) != 2 or budget < 1:
         raise ValueError("to_table must be int32 [n_seqs, to_max_pages] and budget at least 1")
     to_width = to_table.shape[1]
-    ttp = _int32_dev(to_table, "to_table", (n, to_width), dev)
+    lp = _plain(lens, "lens", torch.int32, (n,), dev)
+    wp = _plain(weights, "weights", torch.float32, (n, kv_heads, width * KV4_PAGE), dev)
+    ttp = _plain(to_table, "to_table", torch.int32, (n, to_width), dev)
     L = lib()
     with _on(dev):
+        where = pages.device
         if to_lens is None:
-            to_lens = _empty(n, dtype=torch.int32, device=dev)
+            to_lens = _empty((n,), torch.int32, where)
         if kept is None:
-            kept = _empty((n, kv_heads, budget), dtype=torch.int32, device=dev)
+            kept = _empty((n, kv_heads, budget), torch.int32, where)
         if to_weights is None:
-            to_weights = _empty((n, kv_heads, to_width * KV4_PAGE), dtype=torch.float32, device=dev)
-        elif to_weights.dtype != torch.float32 or tuple(to_weights.shape) != (n, kv_heads, to_width * KV4_PAGE) \
-                or to_weights.device != dev:
-            raise ValueError("to_weights must be fp32 [n_seqs, kv_heads, to_max_pages * 64]")
-        if workspace is None:
-            workspace = _empty(max(256, L.vlm_kv4_evict_workspace_size(pages.shape[0], n, kv_heads, budget)),
-                               dtype=torch.uint8, device=dev)
-        if status is None:
-            status = new_status(dev)
-        _check(L.vlm_kv4_evict(desc, tp, width, n, _int32_dev(lens, "lens", (n,), dev), _dev(weights, "weights"),
-                               budget, int(sinks), int(recent), ttp, to_width,
-                               _int32_dev(to_lens, "to_lens", (n,), dev), _dev(to_weights, "to_weights"),
-                               _int32_dev(kept, "kept", (n, kv_heads, budget), dev), _dev(workspace, "workspace"),
-                               workspace.numel(), _dev(status, "status"), _stream(stream)), "vlm_kv4_evict")
+            to_weights = _empty((n, kv_heads, to_width * KV4_PAGE), torch.float32, where)
+        ws, ws_ptr, ws_bytes = _workspace(workspace, lambda: L.vlm_kv4_evict_workspace_size(pages.shape[0], n, kv_heads,
+                                                                                            budget), dev)
+        _check(L.vlm_kv4_evict(desc, tp, width, n, lp, wp, budget, sinks, recent, ttp, to_width,
+                               _plain(to_lens, "to_lens", torch.int32, (n,), dev),
+                               _plain(to_weights, "to_weights", torch.float32, (n, kv_heads, to_width * KV4_PAGE), dev),
+                               _plain(kept, "kept", torch.int32, (n, kv_heads, budget), dev), ws_ptr, ws_bytes,
+                               _status_ptr(status, dev), _stream_on(dev, stream)), "vlm_kv4_evict")
     return to_lens, kept, to_weights
 
 
