@@ -13,8 +13,10 @@
 //     such tiles for more than 8 rows, further row tiles for more than 16. So
 //     what is made from codes is the big operand, made once in registers, which
 //     tcgen05 cannot take; at these few rows the product is far from its rate.
-//   - A warp takes half pages, 32 tokens, by bulk copies into a ring of its own
-//     in shared memory, so no warp waits for another.
+//   - A warp works on its own run of pages, one bulk copy each into a ring of its
+//     own in shared memory: no warp waits for another, at the ends of runs neither.
+//     With one 8-row tile it takes a page's 64 tokens at once, which gives four
+//     independent chains of products to fill the pipes with.
 //   - Code times block scale has at most 6 significant bits, so fp16 holds it
 //     exactly: one cvt and one multiply per two values, no rounding. A query
 //     row is scaled by a power of two so that its largest value lies in [1, 2)
@@ -24,7 +26,7 @@
 //     log2(e) are one fp32 factor of the logit.
 //   - P is rounded to fp16 for the second product (half a step, 2^-11); the
 //     sum of a row's weights, its maximum and both products' sums stay in fp32.
-//   - Work is cut into equal runs of pages over the flattened (sequence, key
+//   - Work is cut into equal runs of pages, one per warp, over the flattened (sequence, key
 //     head, row tile, page) list, whatever the lengths, computed on the device
 //     from the lengths there, so a captured graph replays with other lengths.
 //     A unit (sequence, key head, row tile) cut by a border leaves partial sums
@@ -46,13 +48,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kPart = 32;  // tokens of a page that a warp takes at a time
+constexpr int kJoinThreads = 256;  // of the kernel that joins cut units
 constexpr int kMaxSeqs = 4096;  // sequences per launch (their page offsets are held in shared memory)
-constexpr int kMaxCtasPerSm = 4;
-// registers: O and q take 48 per lane for one 8-row tile, 96 for two
-template <int NT>
-constexpr int kCtasPerSm = NT == 1 ? 4 : 3;
-constexpr int kMinPages = 4;  // a run shorter than this costs more to join than it gains
+constexpr int kCtasPerSm = 3;  // 168 registers; four CTAs would have to spill
+constexpr int kMinPages = 1;  // a run shorter than this costs more to join than it gains
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNoMax = -3.0e38f;  // a row's maximum before it sees a place; finite, so that -inf minus it is no NaN
 constexpr float kRescale = 8.0f;  // log2 units; P stays below 2^8
@@ -83,11 +82,11 @@ struct Args {
   float scale;
   void* out;         // [n_seqs * q_len, heads, D]
   int32_t* prefix;   // [n_seqs + 1] page offsets, written by the first kernel's CTA 0
-  float* part_o;     // [2 * grid][16][D]
-  float2* part_ml;   // [2 * grid][16] maximum (log2 units) and sum
+  float* part_o;     // [2 * runs][tile_rows][D]
+  float2* part_ml;   // [2 * runs][tile_rows] maximum (log2 units) and sum
   float* lse;        // [n_seqs, kv_heads, rows] log2 of a row's sum (null: not wanted)
   float* weights;    // [n_seqs, kv_heads, max_pages * 64]
-  int grid;          // CTAs of the first kernel
+  int runs;          // warps of the first kernel
   int32_t* status;
 };
 
@@ -104,11 +103,8 @@ struct Map {
   static constexpr int kX = D == 128 ? 1 : 2;
   static constexpr int kSteps = D / 16;  // mma steps of a logit
   static constexpr int kCols = D / 4;    // columns per lane
-  // a ring slot: 32 tokens as key codes, value codes, key scales, value scales
-  static constexpr int kV = kPart * D / 2, kKs = 2 * kV, kVs = kKs + kPart * D / 16;
-  static constexpr int kBytes = kVs + kPart * D / 16;
-  static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr int kRing = kStages * kBytes;  // bytes per warp
+  static constexpr int kStages = D == 128 ? 2 : 4;              // pages in a warp's ring
+  static constexpr int kRing = kStages * Kv4Layout<D>::kBytes;  // bytes per warp
   static __device__ __forceinline__ int token(int i, int c, int e) { return 8 * i + 4 * e + (c ^ (kX * e)); }
 };
 
@@ -117,7 +113,7 @@ struct Plan {
 };
 
 // The page offsets of all sequences into shared memory (prefix[n_seqs + 1]) and the cut.
-__device__ __forceinline__ Plan make_plan(const Kv4& c, int units_per_seq, int grid, int* prefix, int* warp_sum,
+__device__ __forceinline__ Plan make_plan(const Kv4& c, int units_per_seq, int runs, int* prefix, int* warp_sum,
                                           int32_t* status) {
   const int n = c.n_seqs, per = (n + kThreads - 1) / kThreads;
   const int lo = min(n, static_cast<int>(threadIdx.x) * per), hi = min(n, lo + per);
@@ -141,7 +137,7 @@ __device__ __forceinline__ Plan make_plan(const Kv4& c, int units_per_seq, int g
   __syncthreads();
   Plan p;
   p.total = static_cast<int64_t>(prefix[n]) * units_per_seq;
-  p.chunk = max(static_cast<int64_t>(kMinPages), (p.total + grid - 1) / grid);
+  p.chunk = max(static_cast<int64_t>(kMinPages), (p.total + runs - 1) / runs);
   return p;
 }
 
@@ -191,36 +187,22 @@ __device__ __forceinline__ void load_q(const Args& a, int s, int kvh, int first,
   }
 }
 
-// The halves of a run's pages that a warp takes, every kWarps-th, through its
-// ring: four bulk copies each, one by each of the lanes 0..3, counted on one
-// barrier. All lanes call together. kWarps is even, so a warp takes the same
-// half of every page and a copy's place inside the page never changes.
+// The pages of a warp's run through its ring, one bulk copy each. All lanes call
+// together, lane 0 issues.
 template <int D>
-struct PartRing {
-  static_assert(kWarps % 2 == 0, "one half per warp");
-  uint32_t bars;        // shared-memory address of the barriers
-  uint32_t dst, bytes;  // this lane's copy: into slot 0, its size
-  uint32_t src;         // its offset in a page
+struct PageRing {
+  uint32_t ring, bars;  // shared-memory addresses
   uint32_t issued = 0, taken = 0;
-  __device__ __forceinline__ PartRing(uint32_t ring, uint32_t bars_, int half, int lane) : bars(bars_) {
-    using M = Map<D>;
-    using L = Kv4Layout<D>;
-    const int which = lane & 1;
-    const bool codes = (lane & 2) == 0;
-    bytes = codes ? M::kV : M::kVs - M::kKs;
-    src = codes ? which * L::kV + half * M::kV : L::kKs + which * (L::kVs - L::kKs) + half * (M::kVs - M::kKs);
-    dst = ring + (codes ? which * M::kV : M::kKs + which * (M::kVs - M::kKs));
-  }
   __device__ __forceinline__ void issue(const uint8_t* page, int lane) {
-    using M = Map<D>;
-    const uint32_t st = issued % M::kStages, bar = bars + st * 8;
-    if (lane == 0) mbar_arrive_expect_tx(bar, M::kBytes);
-    __syncwarp();
-    if (lane < 4)
+    constexpr uint32_t n = Map<D>::kStages, bytes = Kv4Layout<D>::kBytes;
+    const uint32_t st = issued % n, bar = bars + st * 8;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar, bytes);
       asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                       dst + st * M::kBytes),
-                   "l"(page + src), "r"(bytes), "r"(bar)
+                       ring + st * bytes),
+                   "l"(page), "r"(bytes), "r"(bar)
                    : "memory");
+    }
     ++issued;
   }
   __device__ __forceinline__ bool wait(volatile int* abort, int32_t* status) const {
@@ -229,28 +211,30 @@ struct PartRing {
   }
 };
 
-// S^T = (code * scale) . q for the 32 tokens of a ring slot: s[x][n] is 16
-// tokens by 8 query rows.
-template <int D, int NT>
-__device__ __forceinline__ void logits(const uint8_t* part, const uint32_t (&qf)[NT][D / 16][2], float (&s)[2][NT][4]) {
+// S^T = (code * scale) . q for tokens [16 x0, 16 (x0 + X)) of a page in shared
+// memory: s[x][n] is 16 tokens by 8 query rows.
+template <int D, int NT, int X>
+__device__ __forceinline__ void logits(const uint8_t* page, int x0, const uint32_t (&qf)[NT][D / 16][2],
+                                       float (&s)[X][NT][4]) {
   using M = Map<D>;
+  using L = Kv4Layout<D>;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
+  for (int x = 0; x < X; ++x) {
     uint32_t w[2][D / 32], sc[2][D == 128 ? 2 : 1];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int row = 16 * x + M::token(i, g >> 1, g & 1);
+      const int row = 16 * (x0 + x) + M::token(i, g >> 1, g & 1);
       if constexpr (D == 128) {
-        const uint4 u = *reinterpret_cast<const uint4*>(part + row * 64 + c * 16);
+        const uint4 u = *reinterpret_cast<const uint4*>(page + row * 64 + c * 16);
         w[i][0] = u.x; w[i][1] = u.y; w[i][2] = u.z; w[i][3] = u.w;
-        const uint32_t h2 = e4m3x2_f16(*reinterpret_cast<const uint16_t*>(part + M::kKs + row * 8 + 2 * c));
+        const uint32_t h2 = e4m3x2_f16(*reinterpret_cast<const uint16_t*>(page + L::kKs + row * 8 + 2 * c));
         sc[i][0] = __byte_perm(h2, 0, 0x1010);
         sc[i][1] = __byte_perm(h2, 0, 0x3232);
       } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(part + row * 32 + c * 8);
+        const uint2 u = *reinterpret_cast<const uint2*>(page + row * 32 + c * 8);
         w[i][0] = u.x; w[i][1] = u.y;
-        const uint32_t h2 = e4m3x2_f16(part[M::kKs + row * 4 + c]);
+        const uint32_t h2 = e4m3x2_f16(page[L::kKs + row * 4 + c]);
         sc[i][0] = __byte_perm(h2, 0, 0x1010);
       }
     }
@@ -293,19 +277,12 @@ __device__ __forceinline__ Place place_of(const int* prefix, int n_seqs, int kv_
   p.s = lo;
   p.pages = prefix[lo + 1] - prefix[lo];
   const int64_t r = x - static_cast<int64_t>(prefix[lo]) * per_seq;
-  const int unit = static_cast<int>(r / p.pages);
+  const int unit = r < 0x80000000LL ? static_cast<int>(static_cast<uint32_t>(r) / static_cast<uint32_t>(p.pages))
+                                    : static_cast<int>(r / p.pages);
   p.page = static_cast<int>(r - static_cast<int64_t>(unit) * p.pages);
   p.kvh = unit / row_tiles;
   p.tile = unit % row_tiles;
   return p;
-}
-
-// Element (row, column quad) of the O tile a warp leaves in its ring, in
-// floats; the exchange spreads the rows that one store touches over the banks.
-template <int D>
-__device__ __forceinline__ int o_at(int row, int quad) {
-  const int c = row >> 1;
-  return row * D + ((quad ^ (D == 128 ? c & 3 : (c & 1) | ((c & 2) << 1))) * 4);
 }
 
 template <typename T>
@@ -323,21 +300,22 @@ struct State {
   uint64_t l[NT];
 };
 
-// The 32 tokens of a ring slot, from place `first` on, into the state.
-template <int D, int NT, bool kEdge>
-__device__ __forceinline__ void take32(const uint8_t* part, int first, int len, const int (&seen)[NT][2],
-                                       const uint32_t (&qf)[NT][D / 16][2], const float (&factor)[NT][2],
-                                       State<D, NT>& z) {
+// Tokens [16 x0, 16 (x0 + X)) of a page whose first place is `first` into the state.
+template <int D, int NT, int X, bool kEdge>
+__device__ __forceinline__ void take(const uint8_t* page, int x0, int first, int len, const int (&seen)[NT][2],
+                                     const uint32_t (&qf)[NT][D / 16][2], const float (&factor)[NT][2],
+                                     State<D, NT>& z) {
   using M = Map<D>;
+  using L = Kv4Layout<D>;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  float s[2][NT][4];
-  logits<D, NT>(part, qf, s);
+  float s[X][NT][4];
+  logits<D, NT, X>(page, x0, qf, s);
   if (kEdge) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < X; ++x)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int j = first + 16 * x + M::token(e >> 1, g >> 1, g & 1);
+        const int j = first + 16 * (x0 + x) + M::token(e >> 1, g >> 1, g & 1);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
           if (j >= seen[n][e & 1]) s[x][n][e] = -INFINITY;
@@ -349,7 +327,9 @@ __device__ __forceinline__ void take32(const uint8_t* part, int first, int len, 
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      mx[n][r] = fmaxf(max3f(s[0][n][r], s[0][n][2 + r], s[1][n][r]), s[1][n][2 + r]);
+      mx[n][r] = fmaxf(s[0][n][r], s[0][n][2 + r]);
+#pragma unroll
+      for (int x = 1; x < X; ++x) mx[n][r] = max3f(mx[n][r], s[x][n][r], s[x][n][2 + r]);
       grows |= mx[n][r] > z.grow[n][r];
     }
   if (__any_sync(0xffffffffu, grows)) {
@@ -373,40 +353,40 @@ __device__ __forceinline__ void take32(const uint8_t* part, int first, int len, 
         for (int e = 0; e < 4; ++e) z.o[n][j][e] *= corr[e & 1];
     }
   }
-  uint32_t pf[2][NT][2];
+  uint32_t pf[X][NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const uint64_t f2 = pack2(__float_as_uint(factor[n][0]), __float_as_uint(factor[n][1]));
     const uint64_t negm = pack2(__float_as_uint(-z.m[n][0]), __float_as_uint(-z.m[n][1]));
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < X; ++x)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float x0, x1;
-        unpack2(mul2(add2(pack2(__float_as_uint(s[x][n][2 * i]), __float_as_uint(s[x][n][2 * i + 1])), negm), f2), x0, x1);
-        x0 = ex2(x0);
-        x1 = ex2(x1);
-        z.l[n] = add2(z.l[n], pack2(__float_as_uint(x0), __float_as_uint(x1)));
-        pf[x][n][i] = transpose8(pack_f16x2(x0, x1));
+        float p0, p1;
+        unpack2(mul2(add2(pack2(__float_as_uint(s[x][n][2 * i]), __float_as_uint(s[x][n][2 * i + 1])), negm), f2), p0, p1);
+        p0 = ex2(p0);
+        p1 = ex2(p1);
+        z.l[n] = add2(z.l[n], pack2(__float_as_uint(p0), __float_as_uint(p1)));
+        pf[x][n][i] = transpose8(pack_f16x2(p0, p1));
       }
   }
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
+  for (int x = 0; x < X; ++x) {
     uint32_t vsc[2], v[2][2][D / 64];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint32_t by[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int row = 16 * x + M::token(i, c, e);
-        by[e] = D == 128 ? part[M::kVs + row * 8 + g] : part[M::kVs + row * 4 + (g >> 1)];
+        const int row = 16 * (x0 + x) + M::token(i, c, e);
+        by[e] = D == 128 ? page[L::kVs + row * 8 + g] : page[L::kVs + row * 4 + (g >> 1)];
         if (kEdge && first + row >= len) by[e] = 0;
         if constexpr (D == 128) {
-          const uint2 u = *reinterpret_cast<const uint2*>(part + M::kV + row * 64 + 8 * g);
+          const uint2 u = *reinterpret_cast<const uint2*>(page + L::kV + row * 64 + 8 * g);
           v[i][e][0] = u.x;
           v[i][e][1] = u.y;
         } else {
-          v[i][e][0] = *reinterpret_cast<const uint32_t*>(part + M::kV + row * 32 + 4 * g);
+          v[i][e][0] = *reinterpret_cast<const uint32_t*>(page + L::kV + row * 32 + 4 * g);
         }
       }
       vsc[i] = e4m3x2_f16(by[0] | by[1] << 8);
@@ -434,60 +414,63 @@ __device__ __forceinline__ void take32(const uint8_t* part, int first, int len, 
   }
 }
 
+// A warp's ring, its barriers and the CTA's page offsets, in shared memory.
+template <int D>
+struct Smem {
+  uint64_t bars[kWarps][Map<D>::kStages];
+  int warp_sum[kWarps];
+  int abort_flag;
+};
+template <int D>
+__device__ __forceinline__ void init_smem(Smem<D>& sm, int warp, int lane) {
+  if (lane == 0) {
+    for (int i = 0; i < Map<D>::kStages; ++i) mbar_init(smem_u32(&sm.bars[warp][i]), 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 0) sm.abort_flag = 0;
+}
+
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) kv4_attn_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Args a) {
   using M = Map<D>;
   using L = Kv4Layout<D>;
   constexpr int kTileRows = 8 * NT;
-  static_assert(M::kRing >= kTileRows * D * 4, "a warp's O tile fits its ring");
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int warp_sum[kWarps];
-  __shared__ float sm_m[kWarps][kTileRows], sm_l[kWarps][kTileRows];
-  __shared__ uint64_t bars[kWarps][M::kStages];
-  __shared__ int abort_flag;
+  __shared__ Smem<D> sm;
   int* prefix = reinterpret_cast<int*>(smem + kWarps * M::kRing);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  uint8_t* ring = smem + warp * M::kRing;
-  PartRing<D> pr(smem_u32(ring), smem_u32(bars[warp]), warp & 1, lane);
-  if (lane == 0) {
-    for (int i = 0; i < M::kStages; ++i) mbar_init(smem_u32(&bars[warp][i]), 1);
-    fence_mbar_init();
-  }
-  if (threadIdx.x == 0) abort_flag = 0;
-  volatile int* abort_v = &abort_flag;
+  const uint8_t* ring = smem + warp * M::kRing;
+  PageRing<D> pr{smem_u32(ring), smem_u32(sm.bars[warp])};
+  init_smem(sm, warp, lane);
+  volatile int* abort_v = &sm.abort_flag;
 
   griddep_wait();
   griddep_launch_dependents();
   const int per_seq = a.c.kv_heads * a.row_tiles;
-  const Plan plan = make_plan(a.c, per_seq, a.grid, prefix, warp_sum, blockIdx.x == 0 ? a.status : nullptr);
+  const Plan plan = make_plan(a.c, per_seq, a.runs, prefix, sm.warp_sum, blockIdx.x == 0 ? a.status : nullptr);
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i <= a.c.n_seqs; i += kThreads) a.prefix[i] = prefix[i];
 
   // sequences without a token: their rows are 0
-  for (int s = blockIdx.x; s < a.c.n_seqs; s += a.grid) {
+  for (int s = blockIdx.x; s < a.c.n_seqs; s += gridDim.x) {
     if (prefix[s + 1] != prefix[s]) continue;
     uint2* dst = reinterpret_cast<uint2*>(static_cast<T*>(a.out) + static_cast<int64_t>(s) * a.q_len * a.heads * D);
     for (int i = threadIdx.x; i < a.q_len * a.heads * D / 4; i += kThreads) dst[i] = make_uint2(0, 0);
   }
 
-  bool ok = true;
-  const int64_t begin = blockIdx.x * plan.chunk;
+  // runs go to CTAs in turn, so that few runs spread over the SMs
+  const int run = warp * gridDim.x + blockIdx.x;
+  const int64_t begin = run * plan.chunk;
   const int64_t end = min(plan.total, begin + plan.chunk);
   for (int64_t x = begin; x < end;) {
     const Place at = place_of(prefix, a.c.n_seqs, a.c.kv_heads, a.row_tiles, x);
     const int p0 = at.page;
     const int p1 = static_cast<int>(min(static_cast<int64_t>(at.pages), p0 + (end - x)));
     const int len = kv4_len(a.c, at.s, nullptr);
-
-    // this warp's half pages 2 p0 + warp, + kWarps, ...: two of kWarps = 4 pages' eight;
-    // the page numbers of the next 32 of them, one per lane
-    const int mine = (2 * (p1 - p0) - warp + kWarps - 1) / kWarps;
-    int ids = 0;
+    const int mine = p1 - p0;
+    int ids = 0;  // the numbers of the next 32 pages, one per lane
     auto issue = [&](int k) {  // k in order, all lanes together
-      if (k % 32 == 0) {
-        const int e = p0 + (warp + (k + lane) * kWarps) / 2;
-        ids = e < p1 ? static_cast<int>(kv4_page(a.c, at.s, e, a.status)) : 0;
-      }
+      if (k % 32 == 0) ids = p0 + k + lane < p1 ? static_cast<int>(kv4_page(a.c, at.s, p0 + k + lane, a.status)) : 0;
       pr.issue(a.c.pages + (static_cast<int64_t>(__shfl_sync(0xffffffffu, ids, k % 32)) * a.c.kv_heads + at.kvh) * L::kBytes,
                lane);
     };
@@ -515,25 +498,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) kv4_attn_kernel(cons
         for (int e = 0; e < 4; ++e) z.o[n][j][e] = 0.0f;
     }
 
-    for (int k = 0; k < mine; ++k) {
-      if (ok) ok = pr.wait(abort_v, a.status);
-      const uint8_t* part = ring + pr.taken % M::kStages * M::kBytes;
-      const int first = p0 * kKv4Page + (warp + k * kWarps) * kPart;
-      if (ok) {
-        if (first + kPart <= open)
-          take32<D, NT, false>(part, first, len, seen, qf, factor, z);
-        else
-          take32<D, NT, true>(part, first, len, seen, qf, factor, z);
+    bool ok = true;
+    for (int k = 0; k < mine && ok; ++k) {
+      ok = pr.wait(abort_v, a.status);
+      if (!ok) break;
+      const uint8_t* page = ring + pr.taken % M::kStages * L::kBytes;
+      const int first = (p0 + k) * kKv4Page;
+      // a whole page at once, or halves where two row tiles' state takes the registers
+      constexpr int X = NT == 1 ? 4 : 2;
+#pragma unroll 1
+      for (int x0 = 0; x0 < 4; x0 += X) {
+        if (first + kKv4Page <= open)
+          take<D, NT, X, false>(page, x0, first, len, seen, qf, factor, z);
+        else if (first + 16 * x0 < len)
+          take<D, NT, X, true>(page, x0, first, len, seen, qf, factor, z);
       }
       ++pr.taken;
       __syncwarp();
-      if (ok && next < mine) {
+      if (next < mine) {
         issue(next);
         ++next;
       }
     }
-    // join the four warps: a common maximum per row (in log2 units), each warp's O in its ring
-    float m[NT][2];
+    if (!ok) break;  // a copy that never arrived: the status word says so
+
+    // the rows' results, or partial sums where the unit goes on in other runs
+    const bool whole = p0 == 0 && p1 == at.pages;
+    const int64_t slot = 2 * static_cast<int64_t>(run) + (x == begin ? 0 : 1);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float l[2];
@@ -542,125 +533,113 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) kv4_attn_kernel(cons
       for (int r = 0; r < 2; ++r) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-        m[n][r] = z.m[n][r] == kNoMax ? -INFINITY : z.m[n][r] * factor[n][r];
-        if (g == 0) {
-          sm_m[warp][8 * n + 2 * c + r] = m[n][r];
-          sm_l[warp][8 * n + 2 * c + r] = l[r];
-        }
-      }
-    }
-    __syncthreads();
-    float* own = reinterpret_cast<float*>(ring);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = 8 * n + 2 * c + r;
-        float top = sm_m[0][row];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm_m[w][row]);
-        const float f = m[n][r] == top ? 1.0f : ex2(m[n][r] - top);
+        const int tr = 8 * n + 2 * c + r, row = at.tile * kTileRows + tr;
+        if (row >= a.rows) continue;
+        const float m = z.m[n][r] == kNoMax ? -INFINITY : z.m[n][r] * factor[n][r];  // log2 units
         // columns g D / 8 + 2 j (elements r) and + 1 (elements 2 + r) of tile j
+        if (whole) {
+          const float inv = l[r] == 0.0f ? 0.0f : a.c.v_sg / l[r];
+          T* dst = static_cast<T*>(a.out) +
+                   ((static_cast<int64_t>(at.s) * a.q_len + row / a.group) * a.heads + at.kvh * a.group + row % a.group) * D +
+                   g * (D / 8);
 #pragma unroll
-        for (int j = 0; j < D / 16; j += 2)
-          *reinterpret_cast<float4*>(own + o_at<D>(row, g * (D / 32) + j / 2)) =
-              make_float4(z.o[n][j][r] * f, z.o[n][j][2 + r] * f, z.o[n][j + 1][r] * f, z.o[n][j + 1][2 + r] * f);
-      }
-    __syncthreads();
-    const bool whole = p0 == 0 && p1 == at.pages;
-    const int slot = 2 * blockIdx.x + (x == begin ? 0 : 1);
-    {
-      constexpr int kPer = kThreads / kTileRows;  // threads per row
-      const int r = threadIdx.x / kPer, part = threadIdx.x % kPer;
-      const int row = at.tile * kTileRows + r;
-      if (row < a.rows) {
-        float top = sm_m[0][r], sum = 0.0f;
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm_m[w][r]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += sm_l[w][r] * (sm_m[w][r] == top ? 1.0f : ex2(sm_m[w][r] - top));
-        const float inv = sum == 0.0f ? 0.0f : a.c.v_sg / sum;
-        T* dst = static_cast<T*>(a.out) +
-                 ((static_cast<int64_t>(at.s) * a.q_len + row / a.group) * a.heads + at.kvh * a.group + row % a.group) * D;
-#pragma unroll
-        for (int k = 0; k < D / 4 / kPer; ++k) {
-          const int quad = part + kPer * k;
-          float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float4 u = *reinterpret_cast<const float4*>(
-                reinterpret_cast<const float*>(smem + w * M::kRing) + o_at<D>(r, quad));
-            t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
-          }
-          if (whole)
-            store4<T>(dst + quad * 4, t.x * inv, t.y * inv, t.z * inv, t.w * inv);
-          else
-            *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(slot) * 16 + r) * D + quad * 4) = t;
-        }
-        if (part == 0) {
-          if (!whole) a.part_ml[slot * 16 + r] = make_float2(top, sum);
-          if (whole && a.lse != nullptr)
+          for (int j = 0; j < D / 16; j += 4)
+            *reinterpret_cast<uint4*>(dst + 2 * j) =
+                make_uint4(pack16<T>(z.o[n][j][r] * inv, z.o[n][j][2 + r] * inv),
+                           pack16<T>(z.o[n][j + 1][r] * inv, z.o[n][j + 1][2 + r] * inv),
+                           pack16<T>(z.o[n][j + 2][r] * inv, z.o[n][j + 2][2 + r] * inv),
+                           pack16<T>(z.o[n][j + 3][r] * inv, z.o[n][j + 3][2 + r] * inv));
+          if (g == 0 && a.lse != nullptr)
             a.lse[(static_cast<int64_t>(at.s) * a.c.kv_heads + at.kvh) * a.rows + row] =
-                sum == 0.0f ? INFINITY : top + log2f(sum);
+                l[r] == 0.0f ? INFINITY : m + log2f(l[r]);
+        } else {
+          float* dst = a.part_o + (slot * kTileRows + tr) * D + g * (D / 8);
+#pragma unroll
+          for (int j = 0; j < D / 16; j += 2)
+            *reinterpret_cast<float4*>(dst + 2 * j) =
+                make_float4(z.o[n][j][r], z.o[n][j][2 + r], z.o[n][j + 1][r], z.o[n][j + 1][2 + r]);
+          if (g == 0) a.part_ml[slot * kTileRows + tr] = make_float2(m, l[r]);
         }
       }
     }
-    fence_proxy_async_smem();  // the O tiles were written where the next pages will be copied
-    __syncthreads();
     x += p1 - p0;
   }
 }
 
-// Joins the partial sums of one row of a unit that was cut: a CTA per row,
-// the runs strided over its warps, each lane four columns.
+// Joins the partial sums of one row of a unit that was cut: a CTA per row. All
+// the runs' factors first, one run per thread, then their O rows strided over
+// the warps, each lane four columns, eight loads under way at a time.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) kv4_combine_kernel(const Args a) {
+__global__ void __launch_bounds__(kJoinThreads) kv4_combine_kernel(const Args a) {
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ float sm_o[kWarps][D];
-  __shared__ float2 sm_ml[kWarps];
+  constexpr int kJoinWarps = kJoinThreads / 32;
+  __shared__ float sm_o[kJoinWarps][D];
+  __shared__ float factor[kJoinThreads];
+  __shared__ float sm_red[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.y, tile = row / a.tile_rows, r = row % a.tile_rows;
   const int s = blockIdx.x / a.c.kv_heads, kvh = blockIdx.x % a.c.kv_heads;
   const int per_seq = a.c.kv_heads * a.row_tiles;
   const int64_t total = static_cast<int64_t>(a.prefix[a.c.n_seqs]) * per_seq;
-  const int64_t chunk = max(static_cast<int64_t>(kMinPages), (total + a.grid - 1) / a.grid);
+  const int64_t chunk = max(static_cast<int64_t>(kMinPages), (total + a.runs - 1) / a.runs);
   const int pages = a.prefix[s + 1] - a.prefix[s];
   const int64_t lo = static_cast<int64_t>(a.prefix[s]) * per_seq + static_cast<int64_t>(kvh * a.row_tiles + tile) * pages;
-  const int64_t i0 = lo / chunk, i1 = (lo + pages - 1) / chunk;
+  const int i0 = static_cast<int>(lo / chunk), i1 = static_cast<int>((lo + pages - 1) / chunk);
   float* lse = a.lse == nullptr ? nullptr : a.lse + (static_cast<int64_t>(s) * a.c.kv_heads + kvh) * a.rows + row;
   if (pages == 0) {
     if (lse != nullptr && threadIdx.x == 0) *lse = INFINITY;
     return;
   }
   if (i0 == i1) return;  // one run held the unit: done there
-  auto slot = [&](int64_t i) { return 2 * i + (i * chunk >= lo ? 0 : 1); };
-  float top = -INFINITY;
-  for (int64_t i = i0 + lane; i <= i1; i += 32) top = fmaxf(top, a.part_ml[slot(i) * 16 + r].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  // the run that the unit starts in may hold another unit before it
+  auto at = [&](int i) {
+    return (2 * static_cast<int64_t>(i) + (i * chunk >= lo ? 0 : 1)) * a.tile_rows + r;
+  };
+  float top = -INFINITY, sum = 0.0f;
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.0f;
   const bool mine = lane * 4 < D;
-#pragma unroll 4
-  for (int64_t i = i0 + warp; i <= i1; i += kWarps) {
-    const float2 ml = a.part_ml[slot(i) * 16 + r];
-    const float f = ml.x == top ? 1.0f : ex2(ml.x - top);
-    sum += ml.y * f;
+  for (int base = i0; base <= i1; base += kJoinThreads) {  // as a rule once
+    const int n = min(kJoinThreads, i1 - base + 1);
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (static_cast<int>(threadIdx.x) < n) ml = a.part_ml[at(base + threadIdx.x)];
+    float m = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    __syncthreads();
+    if (lane == 0) sm_red[warp] = m;
+    __syncthreads();
+    m = top;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, sm_red[w]);
+    const float rescale = top == m ? 1.0f : ex2(top - m);
+    const float f = ml.x == m ? 1.0f : ex2(ml.x - m);
+    factor[threadIdx.x] = f;
+    top = m;
+    sum = sum * rescale + ml.y * f;
+    t.x *= rescale; t.y *= rescale; t.z *= rescale; t.w *= rescale;
+    __syncthreads();
     if (mine) {
-      const float4 u = *reinterpret_cast<const float4*>(a.part_o + (slot(i) * 16 + r) * D + lane * 4);
-      t.x += u.x * f; t.y += u.y * f; t.z += u.z * f; t.w += u.w * f;
+#pragma unroll 8
+      for (int i = warp; i < n; i += kJoinWarps) {
+        const float4 u = *reinterpret_cast<const float4*>(a.part_o + at(base + i) * D + lane * 4);
+        const float g = factor[i];
+        t.x += u.x * g; t.y += u.y * g; t.z += u.z * g; t.w += u.w * g;
+      }
     }
   }
   if (mine) *reinterpret_cast<float4*>(&sm_o[warp][lane * 4]) = t;
-  if (lane == 0) sm_ml[warp].y = sum;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  __syncthreads();
+  if (lane == 0) sm_red[warp] = sum;
   __syncthreads();
   if (warp != 0) return;
   sum = 0.0f;
   t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    sum += sm_ml[w].y;
+  for (int w = 0; w < kJoinWarps; ++w) {
+    sum += sm_red[w];
     if (mine) {
       const float4 u = *reinterpret_cast<const float4*>(&sm_o[w][lane * 4]);
       t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
@@ -669,9 +648,9 @@ __global__ void __launch_bounds__(kThreads) kv4_combine_kernel(const Args a) {
   const float inv = sum == 0.0f ? 0.0f : a.c.v_sg / sum;
   if (mine)
     store4<T>(static_cast<T*>(a.out) +
-                     ((static_cast<int64_t>(s) * a.q_len + row / a.group) * a.heads + kvh * a.group + row % a.group) * D +
-                     lane * 4,
-                 t.x * inv, t.y * inv, t.z * inv, t.w * inv);
+                  ((static_cast<int64_t>(s) * a.q_len + row / a.group) * a.heads + kvh * a.group + row % a.group) * D +
+                  lane * 4,
+              t.x * inv, t.y * inv, t.z * inv, t.w * inv);
   if (lse != nullptr && lane == 0) *lse = sum == 0.0f ? INFINITY : top + log2f(sum);
 }
 
@@ -680,34 +659,37 @@ __global__ void __launch_bounds__(kThreads) kv4_combine_kernel(const Args a) {
 // kernel would cost 8 bytes per row and token). One warp owns a slice and sums
 // its rows in a fixed order, so no atomics.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) kv4_weights_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_weights_kernel(const Args a) {
   using M = Map<D>;
   using L = Kv4Layout<D>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int warp_sum[kWarps];
-  __shared__ uint64_t bars[kWarps][M::kStages];
-  __shared__ int abort_flag;
+  __shared__ Smem<D> sm;
   int* prefix = reinterpret_cast<int*>(smem + kWarps * M::kRing);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  uint8_t* ring = smem + warp * M::kRing;
-  PartRing<D> pr(smem_u32(ring), smem_u32(bars[warp]), warp & 1, lane);
-  if (lane == 0) {
-    for (int i = 0; i < M::kStages; ++i) mbar_init(smem_u32(&bars[warp][i]), 1);
-    fence_mbar_init();
-  }
-  if (threadIdx.x == 0) abort_flag = 0;
-  volatile int* abort_v = &abort_flag;
-  bool ok = true;
+  const uint8_t* ring = smem + warp * M::kRing;
+  PageRing<D> pr{smem_u32(ring), smem_u32(sm.bars[warp])};
+  init_smem(sm, warp, lane);
+  volatile int* abort_v = &sm.abort_flag;
   griddep_wait();
   griddep_launch_dependents();
-  const Plan plan = make_plan(a.c, a.c.kv_heads, gridDim.x, prefix, warp_sum, nullptr);
-  const int64_t begin = blockIdx.x * plan.chunk;
+  const Plan plan = make_plan(a.c, a.c.kv_heads, a.runs, prefix, sm.warp_sum, nullptr);
+  const int run = warp * gridDim.x + blockIdx.x;
+  const int64_t begin = run * plan.chunk;
   const int64_t end = min(plan.total, begin + plan.chunk);
   for (int64_t x = begin; x < end;) {
     const Place at = place_of(prefix, a.c.n_seqs, a.c.kv_heads, 1, x);
     const int p0 = at.page;
     const int p1 = static_cast<int>(min(static_cast<int64_t>(at.pages), p0 + (end - x)));
     const int len = kv4_len(a.c, at.s, nullptr);
+    const int mine = p1 - p0;
+    int ids = 0;  // the numbers of the next 32 pages, one per lane
+    auto issue = [&](int k) {  // k in order, all lanes together
+      if (k % 32 == 0) ids = p0 + k + lane < p1 ? static_cast<int>(kv4_page(a.c, at.s, p0 + k + lane, a.status)) : 0;
+      pr.issue(a.c.pages + (static_cast<int64_t>(__shfl_sync(0xffffffffu, ids, k % 32)) * a.c.kv_heads + at.kvh) * L::kBytes,
+               lane);
+    };
+    int next = 0;
+    for (; next < min(mine, M::kStages); ++next) issue(next);
     const int open = len - a.q_len + 1;
     const float* lse = a.lse + (static_cast<int64_t>(at.s) * a.c.kv_heads + at.kvh) * a.rows;
     float* dst = a.weights + (static_cast<int64_t>(at.s) * a.c.kv_heads + at.kvh) * a.c.max_pages * kKv4Page;
@@ -726,58 +708,60 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) kv4_weights_kernel(c
         }
     };
     rows_of(0);
-    const int mine = (2 * (p1 - p0) - warp + kWarps - 1) / kWarps;
-    int ids = 0;
-    auto issue = [&](int k) {
-      if (k % 32 == 0) {
-        const int e = p0 + (warp + (k + lane) * kWarps) / 2;
-        ids = e < p1 ? static_cast<int>(kv4_page(a.c, at.s, e, a.status)) : 0;
-      }
-      pr.issue(a.c.pages + (static_cast<int64_t>(__shfl_sync(0xffffffffu, ids, k % 32)) * a.c.kv_heads + at.kvh) * L::kBytes,
-               lane);
-    };
-    int next = 0;
-    for (; next < min(mine, M::kStages); ++next) issue(next);
+    bool ok = true;
     for (int k = 0; k < mine; ++k) {
-      if (ok) ok = pr.wait(abort_v, a.status);
-      const uint8_t* part = ring + pr.taken % M::kStages * M::kBytes;
-      const int first = p0 * kKv4Page + (warp + k * kWarps) * kPart;
-      if (ok && first < len) {
+      // each lane adds to two of the 64 places: tokens g and g + 8 (by c & 1) of tiles c >> 1 and 2 + (c >> 1)
+      const int first = (p0 + k) * kKv4Page;
+      int j_own[2];
+      float before[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        j_own[h] = first + 32 * h + 16 * (c >> 1) + M::token(c & 1, g >> 1, g & 1);
+        before[h] = j_own[h] < len ? dst[j_own[h]] : 0.0f;
+      }
+      ok = pr.wait(abort_v, a.status);
+      if (!ok) break;
+      const uint8_t* page = ring + pr.taken % M::kStages * L::kBytes;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (first + 32 * h >= len) continue;
         float w[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // tokens g and g + 8 of both tiles
         for (int tile = 0; tile < a.row_tiles; ++tile) {
           if (a.row_tiles > 1) rows_of(tile);
           float s[2][NT][4];
-          logits<D, NT>(part, qf, s);
+          logits<D, NT, 2>(page, 2 * h, qf, s);
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
+          for (int y = 0; y < 2; ++y)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int j = first + 16 * x + M::token(e >> 1, g >> 1, g & 1);
+              const int j = first + 32 * h + 16 * y + M::token(e >> 1, g >> 1, g & 1);
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
-                const float p2 = ex2(__fmul_rn(s[x][n][e], factor[n][e & 1]) - norm[n][e & 1]);
-                w[x][e >> 1] += j < seen[n][e & 1] ? p2 : 0.0f;
+                const float p2 = ex2(__fmul_rn(s[y][n][e], factor[n][e & 1]) - norm[n][e & 1]);
+                w[y][e >> 1] += j < seen[n][e & 1] ? p2 : 0.0f;
               }
             }
         }
+        float own = 0.0f;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float v = w[x][i];
+            float v = w[y][i];
             v += __shfl_xor_sync(0xffffffffu, v, 1);
             v += __shfl_xor_sync(0xffffffffu, v, 2);
-            const int j = first + 16 * x + M::token(i, g >> 1, g & 1);
-            if (c == 2 * x + i && j < len) dst[j] += v;
+            if (c == 2 * y + i) own = v;
           }
+        if (j_own[h] < len) dst[j_own[h]] = before[h] + own;
       }
       ++pr.taken;
       __syncwarp();
-      if (ok && next < mine) {
+      if (next < mine) {
         issue(next);
         ++next;
       }
     }
+    if (!ok) break;
     x += p1 - p0;
   }
 }
@@ -802,11 +786,30 @@ bool smem_ready() {
 
 }  // namespace
 
+namespace {
+// One 8-row tile holds the rows, or tiles of 16 (two of 8 that share the
+// operand made from codes); the CTAs; the workspace's parts.
+struct Shape {
+  int tile_rows, grid, seqs;
+  size_t prefix, part_o, part_ml, lse;
+  size_t total() const { return prefix + part_o + part_ml + lse; }
+};
+Shape shape_of(int n_seqs, int heads, int rows, int head_dim, int q_len) {
+  Shape z;
+  z.tile_rows = rows <= 8 ? 8 : 16;
+  z.grid = kCtasPerSm * num_sms();
+  z.seqs = std::min(n_seqs, kMaxSeqs);
+  const size_t slots = 2 * static_cast<size_t>(z.grid) * kWarps * z.tile_rows;
+  z.prefix = up((static_cast<size_t>(z.seqs) + 1) * 4);
+  z.part_o = up(slots * head_dim * 4);
+  z.part_ml = up(slots * 8);
+  z.lse = up(static_cast<size_t>(z.seqs) * heads * q_len * 4);
+  return z;
+}
+}  // namespace
+
 size_t kv4_attention_workspace(int n_seqs, int heads, int kv_heads, int head_dim, int q_len) {
-  (void)kv_heads;
-  const size_t n = std::min(n_seqs, kMaxSeqs);
-  const size_t slots = 2 * static_cast<size_t>(kMaxCtasPerSm) * 256;  // 256: above any SM count
-  return up((n + 1) * 4) + up(slots * 16 * head_dim * 4) + up(slots * 16 * 8) + up(n * heads * q_len * 4);
+  return shape_of(n_seqs, heads, heads / kv_heads * q_len, head_dim, q_len).total();
 }
 
 int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int dtype, const void* q, int64_t q_stride,
@@ -817,25 +820,21 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
   a.group = heads / c0.kv_heads;
   a.q_len = q_len;
   a.rows = a.group * q_len;
-  // one 8-row tile holds the rows, or tiles of 16 (two of 8 that share the operand made from codes)
-  const bool one = a.rows <= 8;
-  a.tile_rows = one ? 8 : 16;
+  const Shape z = shape_of(c0.n_seqs, heads, a.rows, head_dim, q_len);
+  const bool one = z.tile_rows == 8;
+  a.tile_rows = z.tile_rows;
   a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
   a.scale = scale;
-  a.grid = (one ? kCtasPerSm<1> : kCtasPerSm<2>) * std::min(num_sms(), 256);
+  const int grid = z.grid;
+  a.runs = grid * kWarps;
   a.status = status;
-  const size_t slots = 2 * static_cast<size_t>(kMaxCtasPerSm) * 256;
-  const int n_max = std::min(c0.n_seqs, kMaxSeqs);
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.prefix = reinterpret_cast<int32_t*>(w);
-  w += up((static_cast<size_t>(n_max) + 1) * 4);
-  a.part_o = reinterpret_cast<float*>(w);
-  w += up(slots * 16 * head_dim * 4);
-  a.part_ml = reinterpret_cast<float2*>(w);
-  w += up(slots * 16 * 8);
-  a.lse = weights == nullptr ? nullptr : reinterpret_cast<float*>(w);
+  a.part_o = reinterpret_cast<float*>(w + z.prefix);
+  a.part_ml = reinterpret_cast<float2*>(w + z.prefix + z.part_o);
+  a.lse = weights == nullptr ? nullptr : reinterpret_cast<float*>(w + z.prefix + z.part_o + z.part_ml);
   const size_t smem = kWarps * (head_dim == 128 ? Map<128>::kRing : Map<64>::kRing) +
-                      (static_cast<size_t>(n_max) + 1) * 4;
+                      (static_cast<size_t>(z.seqs) + 1) * 4;
   auto run = [&](auto attn, auto combine, auto weigh, int elem, bool ready) -> int {
     if (!ready) return VLM_ERR_CUDA;
     for (int first = 0; first < c0.n_seqs; first += kMaxSeqs) {
@@ -848,10 +847,10 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
       a.weights = weights == nullptr
                       ? nullptr
                       : weights + static_cast<int64_t>(first) * c0.kv_heads * c0.max_pages * kKv4Page;
-      cudaError_t e = launch_pdl(attn, dim3(a.grid), dim3(kThreads), smem, s, a);
+      cudaError_t e = launch_pdl(attn, dim3(grid), dim3(kThreads), smem, s, a);
       if (e == cudaSuccess)
-        e = launch_pdl(combine, dim3(a.c.n_seqs * a.c.kv_heads, a.rows), dim3(kThreads), 0, s, a);
-      if (e == cudaSuccess && weights != nullptr) e = launch_pdl(weigh, dim3(a.grid), dim3(kThreads), smem, s, a);
+        e = launch_pdl(combine, dim3(a.c.n_seqs * a.c.kv_heads, a.rows), dim3(kJoinThreads), 0, s, a);
+      if (e == cudaSuccess && weights != nullptr) e = launch_pdl(weigh, dim3(grid), dim3(kThreads), smem, s, a);
       if (e != cudaSuccess) return VLM_ERR_CUDA;
     }
     return VLM_OK;
