@@ -809,11 +809,13 @@ def _stream_on(dev: int, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _status_ptr(status: torch.Tensor | None, dev: int) -> int:
-    """The caller's status word; without one a word of this call's own, which nobody reads."""
-    if status is None:
-        status = new_status(torch.device("cuda", dev))
-    return _plain(status, "status", torch.int32, (1,), dev)
+def _new(shape, dtype: torch.dtype, where, stream) -> torch.Tensor:
+    """A buffer for a call; one that runs on a given stream keeps the buffer's memory until it is done there."""
+    t = _empty(shape, dtype, where)
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream(t.device))  # whoever had the memory before
+        t.record_stream(stream)
+    return t
 
 
 def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_lens, kv_lens=None,
@@ -823,7 +825,8 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_lens, 
     q [sum(q_lens), heads, head_dim], k and v [sum(kv_lens), kv_heads, head_dim]: bf16 or fp16, any
     stride between tokens (column blocks of one projection's output). q_lens, kv_lens: host lists;
     kv_lens None: the same. The last query of a sequence sees every key. scale None:
-    1 / sqrt(head_dim). Returns out [sum(q_lens), heads, head_dim]."""
+    1 / sqrt(head_dim). Returns out [sum(q_lens), heads, head_dim]. Without a status word (here
+    and in the kv4 calls) errors found on the device go unreported."""
     n = len(q_lens)
     if kv_lens is None:
         kv_lens = q_lens
@@ -842,7 +845,7 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_lens, 
         raise ValueError(f"the lengths add up to {sum(q_lens)} and {sum(kv_lens)}, q has {T} rows and k {tk}")
     with _on(dev):
         if out is None:
-            out = _empty((T, heads, dim), dtype, q.device)
+            out = _new((T, heads, dim), dtype, q.device, stream)
             op, os_ = out.data_ptr(), heads * dim
         else:
             if out.shape != q.shape:
@@ -851,7 +854,7 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_lens, 
         arr = ctypes.c_int32 * max(1, n)
         _check(lib().vlm_prompt_attention(dt, heads, kv_heads, dim, arr(*q_lens), arr(*kv_lens), n, qp, qs, kp, ks,
                                           vp, vs, dim ** -0.5 if scale is None else scale, op, os_,
-                                          _status_ptr(status, dev), _stream_on(dev, stream)), "vlm_prompt_attention")
+                                          _plain(status, "status", torch.int32, (1,), dev), _stream_on(dev, stream)), "vlm_prompt_attention")
     return out
 
 
@@ -902,7 +905,7 @@ def kv4_append(pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor | No
     with _on(dev):
         _check(lib().vlm_kv4_append(desc, tp, width, n, _plain(lens, "lens", torch.int32, (n,), dev),
                                     _plain(cu_new, "cu_new", torch.int32, (n + 1,), dev), n_new, dt, kp, ks, vp, vs,
-                                    _status_ptr(status, dev), _stream_on(dev, stream)), "vlm_kv4_append")
+                                    _plain(status, "status", torch.int32, (1,), dev), _stream_on(dev, stream)), "vlm_kv4_append")
 
 
 def kv4_read(pages: torch.Tensor, table: torch.Tensor, k_sg: float, v_sg: float, cu: torch.Tensor | None, n_rows: int,
@@ -917,13 +920,13 @@ def kv4_read(pages: torch.Tensor, table: torch.Tensor, k_sg: float, v_sg: float,
     shape = (n_rows, kv_heads, dim)
     with _on(dev):
         if k is None:
-            k = _empty(shape, dtype, pages.device)
+            k = _new(shape, dtype, pages.device, stream)
         if v is None:
-            v = _empty(shape, dtype, pages.device)
+            v = _new(shape, dtype, pages.device, stream)
         _check(lib().vlm_kv4_read(desc, tp, width, n, _plain(start, "start", torch.int32, (n,), dev),
                                   _plain(cu, "cu", torch.int32, (n + 1,), dev), n_rows, dt,
                                   _plain(k, "k", dtype, shape, dev), _plain(v, "v", dtype, shape, dev),
-                                  _status_ptr(status, dev), _stream_on(dev, stream)), "vlm_kv4_read")
+                                  _plain(status, "status", torch.int32, (1,), dev), _stream_on(dev, stream)), "vlm_kv4_read")
     return k, v
 
 
@@ -932,10 +935,10 @@ def kv4_attention_workspace_size(n_seqs: int, heads: int, kv_heads: int, head_di
                                                       int(q_len)))
 
 
-def _workspace(ws: torch.Tensor | None, need, dev: int) -> tuple:
+def _workspace(ws: torch.Tensor | None, need, dev: int, stream) -> tuple:
     """(tensor, pointer, bytes) of the caller's uint8 workspace, or of a new one of need() bytes."""
     if ws is None:
-        ws = _empty(max(256, need()), torch.uint8, torch.device("cuda", dev))
+        ws = _new(max(256, need()), torch.uint8, torch.device("cuda", dev), stream)
     elif ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("workspace must be contiguous uint8 on the CUDA device of the other operands")
     return ws, ws.data_ptr(), ws.numel()
@@ -960,13 +963,13 @@ def kv4_attention(pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, 
     L = lib()
     with _on(dev):
         if out is None:
-            out = _empty((T, heads, dim), dtype, pages.device)
+            out = _new((T, heads, dim), dtype, pages.device, stream)
         ws, ws_ptr, ws_bytes = _workspace(workspace, lambda: L.vlm_kv4_attention_workspace_size(n, heads, kv_heads, dim, m),
-                                          dev)
+                                          dev, stream)
         _check(L.vlm_kv4_attention(desc, tp, width, n, _plain(lens, "lens", torch.int32, (n,), dev), dt, heads, m, qp,
                                    qs, dim ** -0.5 if scale is None else scale,
                                    _plain(out, "out", dtype, (T, heads, dim), dev), wp, ws_ptr, ws_bytes,
-                                   _status_ptr(status, dev), _stream_on(dev, stream)), "vlm_kv4_attention")
+                                   _plain(status, "status", torch.int32, (1,), dev), _stream_on(dev, stream)), "vlm_kv4_attention")
     return out
 
 
@@ -992,18 +995,18 @@ def kv4_evict(pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, weig
     with _on(dev):
         where = pages.device
         if to_lens is None:
-            to_lens = _empty((n,), torch.int32, where)
+            to_lens = _new((n,), torch.int32, where, stream)
         if kept is None:
-            kept = _empty((n, kv_heads, budget), torch.int32, where)
+            kept = _new((n, kv_heads, budget), torch.int32, where, stream)
         if to_weights is None:
-            to_weights = _empty((n, kv_heads, to_width * KV4_PAGE), torch.float32, where)
+            to_weights = _new((n, kv_heads, to_width * KV4_PAGE), torch.float32, where, stream)
         ws, ws_ptr, ws_bytes = _workspace(workspace, lambda: L.vlm_kv4_evict_workspace_size(pages.shape[0], n, kv_heads,
-                                                                                            budget), dev)
+                                                                                            budget), dev, stream)
         _check(L.vlm_kv4_evict(desc, tp, width, n, lp, wp, budget, sinks, recent, ttp, to_width,
                                _plain(to_lens, "to_lens", torch.int32, (n,), dev),
                                _plain(to_weights, "to_weights", torch.float32, (n, kv_heads, to_width * KV4_PAGE), dev),
                                _plain(kept, "kept", torch.int32, (n, kv_heads, budget), dev), ws_ptr, ws_bytes,
-                               _status_ptr(status, dev), _stream_on(dev, stream)), "vlm_kv4_evict")
+                               _plain(status, "status", torch.int32, (1,), dev), _stream_on(dev, stream)), "vlm_kv4_evict")
     return to_lens, kept, to_weights
 
 
