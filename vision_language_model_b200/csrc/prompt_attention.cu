@@ -57,7 +57,8 @@ constexpr int HK = BK / 2;     // keys per softmax thread
 constexpr int kSoftWarps = 16;
 constexpr int kThreads = 32 * (4 + kSoftWarps);
 constexpr int kStages = 2;
-constexpr int kMaxSeqs = 256;  // sequences per launch (their table is a kernel argument)
+constexpr int kMaxSeqs = 256;    // sequences per launch (their table is a kernel argument)
+constexpr int kMaxOrder = 1024;  // tiles per key head whose order is passed along
 constexpr int kItemSlots = 512;  // items per CTA and launch
 constexpr int kIssueRegs = 32, kSoftRegs = 112;
 static_assert(128 * kIssueRegs + 32 * kSoftWarps * kSoftRegs <= kThreads * 96, "the launch's registers");
@@ -68,6 +69,8 @@ struct SeqTable {
   int n;
   int off[kMaxSeqs + 1];  // work items before each sequence
   int q0[kMaxSeqs], k0[kMaxSeqs], q_len[kMaxSeqs], kv_len[kMaxSeqs], tiles[kMaxSeqs];  // tiles: items per key head
+  int ordered;               // pairs in `order`, or 0: sequence by sequence, last tile first
+  uint32_t order[kMaxOrder];  // sequence << 16 | tile, the most key tiles first
 };
 
 struct Args {
@@ -202,19 +205,28 @@ struct alignas(16) Item {
   __device__ __forceinline__ int tok(int t, int tpt) const { return tok0 + t * tpt; }
 };
 __device__ __forceinline__ Item item_of(const Args& a, int idx) {
-  int lo = 0, hi = a.t.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.t.off[mid] <= idx) lo = mid; else hi = mid - 1;
-  }
   Item it;
+  int lo = 0, tile;
+  if (a.t.ordered > 0) {
+    const int pair = idx / a.kv_heads;
+    it.head = idx - pair * a.kv_heads;
+    lo = a.t.order[pair] >> 16;
+    tile = a.t.order[pair] & 0xFFFF;
+  } else {
+    int hi = a.t.n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.t.off[mid] <= idx) lo = mid; else hi = mid - 1;
+    }
+    const int r = idx - a.t.off[lo], row = r / a.kv_heads;
+    it.head = r - row * a.kv_heads;
+    tile = a.t.tiles[lo] - 1 - row;
+  }
   it.q0 = a.t.q0[lo];
   it.k0 = a.t.k0[lo];
   it.q_len = a.t.q_len[lo];
   it.kv_len = a.t.kv_len[lo];
-  const int r = idx - a.t.off[lo], row = r / a.kv_heads;
-  it.head = r - row * a.kv_heads;
-  it.tok0 = (a.t.tiles[lo] - 1 - row) * 2 * a.tpt;
+  it.tok0 = tile * 2 * a.tpt;
   it.shift = it.kv_len - it.q_len;
   const int end = it.shift + min(it.q_len, it.tok0 + 2 * a.tpt);  // keys that the last row sees
   it.n = max(0, (end + BK - 1) / BK);
@@ -626,6 +638,31 @@ bool smem_ready() {
   return true;
 }
 
+// Sorts all (sequence, tile) pairs by their key tiles, descending, where few
+// enough of them are passed along: dealt out forwards and backwards they then
+// load the CTAs alike. With more of them every CTA has so many items that the
+// order inside the sequences does. A counting sort: levels are key tiles.
+int order_tiles(SeqTable& t, int tokens, int64_t pairs) {
+  constexpr int kLevels = 4096;
+  if (pairs > kMaxOrder || t.n > 65536) return 0;
+  int most = 0;
+  for (int i = 0; i < t.n; ++i) most = std::max(most, (t.kv_len[i] + BK - 1) / BK);
+  if (most >= kLevels) return 0;
+  auto level = [&](int i, int tile) {
+    const int end = t.kv_len[i] - t.q_len[i] + std::min(t.q_len[i], (tile + 1) * tokens);
+    return end <= 0 ? 0 : (end + BK - 1) / BK;
+  };
+  int start[kLevels + 1];
+  std::fill(start, start + most + 2, 0);
+  for (int i = 0; i < t.n; ++i)
+    for (int x = 0; x < t.tiles[i]; ++x) ++start[most - level(i, x) + 1];
+  for (int l = 0; l < most; ++l) start[l + 1] += start[l];
+  for (int i = 0; i < t.n; ++i)
+    for (int x = t.tiles[i] - 1; x >= 0; --x)
+      t.order[start[most - level(i, x)]++] = static_cast<uint32_t>(i) << 16 | static_cast<uint32_t>(x);
+  return static_cast<int>(pairs);
+}
+
 // Tensor map of 16-bit [tokens, heads, D] with `stride` elements between
 // tokens: 128-byte swizzle, box 64 columns x box_heads x box_tokens.
 bool tmap_3d(CUtensorMap* map, bool half, const void* ptr, int64_t tokens, int heads, int d, int64_t stride,
@@ -691,6 +728,7 @@ int launch_prompt_attention(const PromptAttn& p, cudaStream_t s) {
       }
       if (a.t.n == 0) continue;
       a.t.off[a.t.n] = static_cast<int>(items);
+      a.t.ordered = order_tiles(a.t, 2 * tpt, items / p.kv_heads);
       a.kv_heads = p.kv_heads;
       a.group = group;
       a.tpt = tpt;
