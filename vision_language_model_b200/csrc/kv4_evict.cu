@@ -24,6 +24,7 @@
 // per sequence: marking before comparing lets the CTAs run in any order, of two
 // that meet the later one sees the earlier's mark.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv4.cuh"
 
@@ -349,23 +350,30 @@ __global__ void __launch_bounds__(kMoveThreads) kv4_move_kernel(const EvictArgs 
   }
   __syncthreads();
   uint8_t* dst = a.c.pages + (to * a.c.kv_heads + h) * L::kBytes;
+  // all of a thread's loads before its stores: source and destination are one
+  // buffer, so the compiler would keep each load behind the store before it
   constexpr int kCh = L::kCodeRow / 16;  // 16-byte chunks of a code row
-#pragma unroll 4
-  for (int i = tid; i < rows * kCh * 2; i += kMoveThreads) {
-    const int part = i >= rows * kCh, x = i - part * rows * kCh, r = x / kCh, ch = x % kCh;
-    const int64_t base = part * L::kV + ch * 16;
-    *reinterpret_cast<uint4*>(dst + base + r * L::kCodeRow) =
-        *reinterpret_cast<const uint4*>(a.c.pages + from[r] + base + from_row[r] * L::kCodeRow);
+  constexpr int kEach = kKv4Page * kCh * 2 / kMoveThreads;
+  using Scale = std::conditional_t<D == 128, uint2, uint32_t>;  // a row's scales of keys or values
+  uint4 codes[kEach];
+  Scale scales;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int i = tid + k * kMoveThreads, part = i / (kKv4Page * kCh), x = i % (kKv4Page * kCh), r = x / kCh, ch = x % kCh;
+    if (r < rows)
+      codes[k] = *reinterpret_cast<const uint4*>(a.c.pages + from[r] + part * L::kV + from_row[r] * L::kCodeRow + ch * 16);
   }
-  for (int i = tid; i < rows * 2; i += kMoveThreads) {
-    const int part = i >= rows, r = i - part * rows;
-    const int64_t base = L::kKs + part * (L::kVs - L::kKs);
-    const uint8_t* src = a.c.pages + from[r] + base + from_row[r] * L::kScaleRow;
-    if constexpr (D == 128)
-      *reinterpret_cast<uint2*>(dst + base + r * L::kScaleRow) = *reinterpret_cast<const uint2*>(src);
-    else
-      *reinterpret_cast<uint32_t*>(dst + base + r * L::kScaleRow) = *reinterpret_cast<const uint32_t*>(src);
+  static_assert(kMoveThreads == 2 * kKv4Page, "one scale group per thread");
+  const int s_part = tid / kKv4Page, s_row = tid % kKv4Page;
+  const int64_t s_base = L::kKs + s_part * (L::kVs - L::kKs);
+  if (s_row < rows)
+    scales = *reinterpret_cast<const Scale*>(a.c.pages + from[s_row] + s_base + from_row[s_row] * L::kScaleRow);
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int i = tid + k * kMoveThreads, part = i / (kKv4Page * kCh), x = i % (kKv4Page * kCh), r = x / kCh, ch = x % kCh;
+    if (r < rows) *reinterpret_cast<uint4*>(dst + part * L::kV + r * L::kCodeRow + ch * 16) = codes[k];
   }
+  if (s_row < rows) *reinterpret_cast<Scale*>(dst + s_base + s_row * L::kScaleRow) = scales;
 }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
