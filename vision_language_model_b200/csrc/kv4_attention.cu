@@ -31,7 +31,12 @@
 //     from the lengths there, so a captured graph replays with other lengths.
 //     A unit (sequence, key head, row tile) cut by a border leaves partial sums
 //     that kv4_combine_kernel joins in the order of the runs: the result does
-//     not depend on timing.
+//     not depend on timing (its last bits do on where the batch was cut).
+// Measured, 32/8 heads of 128: 31 sequences of up to 16,000 tokens (378 MB) 78
+// us, of which the first kernel alone 74, 5.1 TB/s (0.78 of the copy rate); what
+// it lacks is issue slots, 58% used, 430 instructions per 32 tokens of a head of
+// which 256 convert and scale. As 16-row tiles of S and O it took 104 us, with
+// fp32 logits stored for the weights they would cost 8 bytes per row and token.
 // Places behind what a row sees get logit -inf; value scales of places behind
 // the sequence's end are taken as 0, so stale bytes (NaN scales among them)
 // reach no sum. A row that sees nothing is 0.
@@ -48,10 +53,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kJoinThreads = 256;  // of the kernel that joins cut units
 constexpr int kMaxSeqs = 4096;  // sequences per launch (their page offsets are held in shared memory)
 constexpr int kCtasPerSm = 3;  // 168 registers; four CTAs would have to spill
-constexpr int kMinPages = 1;  // a run shorter than this costs more to join than it gains
+constexpr int kMinPages = 1;  // of a run: a page takes a warp about 1 us, joining a run less
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNoMax = -3.0e38f;  // a row's maximum before it sees a place; finite, so that -inf minus it is no NaN
 constexpr float kRescale = 8.0f;  // log2 units; P stays below 2^8
@@ -504,8 +508,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Ar
       if (!ok) break;
       const uint8_t* page = ring + pr.taken % M::kStages * L::kBytes;
       const int first = (p0 + k) * kKv4Page;
-      // a whole page at once, or halves where two row tiles' state takes the registers
-      constexpr int X = NT == 1 ? 4 : 2;
+      // a whole page at once, or halves where the state of two row tiles takes the registers
+      constexpr int X = NT == 1 || D == 64 ? 4 : 2;
 #pragma unroll 1
       for (int x0 = 0; x0 < 4; x0 += X) {
         if (first + kKv4Page <= open)
@@ -566,14 +570,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Ar
   }
 }
 
-// Joins the partial sums of one row of a unit that was cut: a CTA per row. All
+// Joins the partial sums of one row of a unit that was cut: a CTA per row, of two
+// warps where a unit has a dozen parts at most, else of eight. All
 // the runs' factors first, one run per thread, then their O rows strided over
 // the warps, each lane four columns, eight loads under way at a time.
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) kv4_combine_kernel(const Args a) {
+template <typename T, int D, int kJoinWarps>
+__global__ void __launch_bounds__(kJoinWarps * 32) kv4_combine_kernel(const Args a) {
   griddep_wait();
   griddep_launch_dependents();
-  constexpr int kJoinWarps = kJoinThreads / 32;
+  constexpr int kJoinThreads = kJoinWarps * 32;
   __shared__ float sm_o[kJoinWarps][D];
   __shared__ float factor[kJoinThreads];
   __shared__ float sm_red[kJoinWarps];
@@ -835,7 +840,7 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
   a.lse = weights == nullptr ? nullptr : reinterpret_cast<float*>(w + z.prefix + z.part_o + z.part_ml);
   const size_t smem = kWarps * (head_dim == 128 ? Map<128>::kRing : Map<64>::kRing) +
                       (static_cast<size_t>(z.seqs) + 1) * 4;
-  auto run = [&](auto attn, auto combine, auto weigh, int elem, bool ready) -> int {
+  auto run = [&](auto attn, auto combine, int join_threads, auto weigh, int elem, bool ready) -> int {
     if (!ready) return VLM_ERR_CUDA;
     for (int first = 0; first < c0.n_seqs; first += kMaxSeqs) {
       a.c = c0;
@@ -849,7 +854,7 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
                       : weights + static_cast<int64_t>(first) * c0.kv_heads * c0.max_pages * kKv4Page;
       cudaError_t e = launch_pdl(attn, dim3(grid), dim3(kThreads), smem, s, a);
       if (e == cudaSuccess)
-        e = launch_pdl(combine, dim3(a.c.n_seqs * a.c.kv_heads, a.rows), dim3(kJoinThreads), 0, s, a);
+        e = launch_pdl(combine, dim3(a.c.n_seqs * a.c.kv_heads, a.rows), dim3(join_threads), 0, s, a);
       if (e == cudaSuccess && weights != nullptr) e = launch_pdl(weigh, dim3(grid), dim3(kThreads), smem, s, a);
       if (e != cudaSuccess) return VLM_ERR_CUDA;
     }
@@ -859,7 +864,9 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
   auto pick = [&](auto type, auto dim, auto nt) {
     using T = decltype(type);
     constexpr int D = decltype(dim)::value, NT = decltype(nt)::value;
-    return run(kv4_attn_kernel<T, D, NT>, kv4_combine_kernel<T, D>, kv4_weights_kernel<T, D, NT>, 2, smem_ready<T, D, NT>());
+    const bool few = a.runs <= 12LL * z.seqs * c0.kv_heads * a.row_tiles;
+    return run(kv4_attn_kernel<T, D, NT>, few ? kv4_combine_kernel<T, D, 2> : kv4_combine_kernel<T, D, 8>, few ? 64 : 256,
+               kv4_weights_kernel<T, D, NT>, 2, smem_ready<T, D, NT>());
   };
   auto by_rows = [&](auto type, auto dim) {
     return one ? pick(type, dim, std::integral_constant<int, 1>()) : pick(type, dim, std::integral_constant<int, 2>());

@@ -9,16 +9,16 @@
 // (row = token * G + head), so both tiles, 2 TPT tokens, share every key and
 // value tile that is loaded, and a short prompt still fills its rows. CTAs
 // (one per SM, 512 TMEM columns) take items in turn, forwards and backwards
-// through the list; the longest sequences and their last tiles come first.
-// 20 warps:
+// through the list, which is sorted by key tiles. 20 warps:
 //   warp 0       TMA: both Q tiles, then K and V tiles of 128 keys into two
 //                2-stage rings (128-byte swizzle, 64-column boxes).
 //   warps 1, 2   issue row tile t's products, one warp each, for key tile j
 //                  S_t  = Q_t K_j^T           (tcgen05.mma kind::f16, M = N = 128)
 //                  O_t += P_t V_{j-1}         (A = P in TMEM, V in smem, MN-major)
-//                Issuing an instruction costs about 90 cycles, the tensor core
-//                needs 64 for it: one warp for both tiles was the bound
-//                (3,520 cycles per key tile at D = 128).
+//                An instruction takes the tensor core 64 cycles. Issued by one
+//                lane of a divergent branch it cost that lane 100, so that one
+//                warp for both tiles was the bound (4,190 cycles per key tile);
+//                as a predicated instruction of a converged warp it costs 65.
 //   warps 4..19  softmax, two threads per row (keys [0, 64) and [64, 128) of
 //                the tile), 256 threads per row tile: running maximum (moved
 //                only when it grows by more than 8 in log2 units), P as 16-bit
@@ -27,6 +27,15 @@
 // Both row tiles take every key tile of the item, so they alternate strictly;
 // the products of key tiles that a row tile does not see at all (one in
 // several) have weight 0.
+// Bound, D = 128: the chain of hand-overs through the shared S buffer. S_0 is
+// copied (250 cycles), handed over (350), S_1's product runs (512) and is
+// reported (430): about 3,200 cycles per key tile against the tensor core's
+// 2,048 and the exponential unit's 1,800. Handing S over in halves of 64 keys
+// (N = 64 products) was slower. D = 64: the softmax itself, 2,700 cycles per key
+// tile. An item costs some 5,000 cycles besides: its last product, O to memory,
+// and the look at V below. Measured, 32/8 heads of 128, bf16: 4,096 tokens 118
+// us, 1,162 TFLOP/s (0.70 of the measured peak); 8,192 tokens 434 us, 1,268;
+// heads of 64: 8,192 tokens 400 us, 690 TFLOP/s.
 // TMEM, D = 128: one S buffer that the row tiles take in turn [0, 128), P
 // [128, 192) and [192, 256), O [256, 384) and [384, 512); a tile's logits leave
 // S for registers at once, so the buffer is free again while its softmax runs.
@@ -488,7 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Logits of ordinary size: 2^(s sl2 - m sl2) in one operation; the rounding of
         // m sl2 scales the row's weights by up to 2^(2^-13) alike. Masked tiles and large
         // logits: subtracted before they are scaled, and no polynomial.
-        const bool plain = !masked && !__any_sync(0xffffffffu, fabsf(ref * args.sl2) > 4096.0f);
+        // (Rows without a token do not vote: they hold other sequences' queries or nothing.)
+        const bool plain = !masked && !__any_sync(0xffffffffu, live && fabsf(ref * args.sl2) > 4096.0f);
         const float sum = plain ? row_exp<true, kHalf>(u, sl2x2, ref * args.sl2, pk)
                                 : row_exp<false, kHalf, true>(u, sl2x2, ref, pk);
         l = l * corr + sum;
