@@ -91,7 +91,13 @@ def test_append_infinities_saturate_and_nan_is_bounded():
     assert float(rk[0, 0, 20]) == pytest.approx(-448 * 6 * K_SG, rel=2 ** -8)
 
 
-def _attend(lens, heads, kv_heads, dim, q_len, dtype, seed=11, weights=False, gain=1.0, width=None):
+def _attend(lens, heads, kv_heads, dim, q_len, dtype, seed=11, weights=False, gain=1.0):
+    """By clusters where the batch is small, and by runs of pages, which a table of more than 128 pages asks for."""
+    _attend_width(lens, heads, kv_heads, dim, q_len, dtype, seed, weights, gain, None)
+    _attend_width(lens, heads, kv_heads, dim, q_len, dtype, seed, weights, gain, 130)
+
+
+def _attend_width(lens, heads, kv_heads, dim, q_len, dtype, seed, weights, gain, width):
     pages, table, _ = U.random_pool(seed, lens, kv_heads, dim, width=width)
     q = U.rand16(seed + 1, (len(lens) * q_len, heads, dim), dtype, gain)
     scale = dim ** -0.5
@@ -128,6 +134,9 @@ def _attend(lens, heads, kv_heads, dim, q_len, dtype, seed=11, weights=False, ga
     ([260, 31], 28, 4, 128, 5),
     ([130, 64], 40, 1, 128, 3),
     ([4000], 2, 1, 128, 1),
+    ([8192, 1], 16, 1, 64, 1),   # as many pages as a small batch may have
+    ([100] * 9, 8, 4, 64, 1),
+    ([100] * 10, 8, 4, 64, 1),   # one unit more than clusters take on a GPU of 148 SMs
 ])
 def test_attention_over_the_cache(lens, heads, kv_heads, dim, q_len, dtype):
     _attend(lens, heads, kv_heads, dim, q_len, dtype, weights=False)

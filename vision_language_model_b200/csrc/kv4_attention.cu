@@ -55,6 +55,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxSeqs = 4096;  // sequences per launch (their page offsets are held in shared memory)
 constexpr int kCtasPerSm = 3;  // 168 registers; four CTAs would have to spill
+constexpr int kCluster = 8;       // CTAs that share a unit of a small batch
+constexpr int kClusterPages = 128;  // and the pages a sequence may then have: four per warp
 constexpr int kMinPages = 1;  // of a run: a page takes a warp about 1 us, joining a run less
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNoMax = -3.0e38f;  // a row's maximum before it sees a place; finite, so that -inf minus it is no NaN
@@ -434,6 +436,36 @@ __device__ __forceinline__ void init_smem(Smem<D>& sm, int warp, int lane) {
   if (threadIdx.x == 0) sm.abort_flag = 0;
 }
 
+template <int D, int NT>
+__device__ __forceinline__ void clear(State<D, NT>& z) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) z.m[n][r] = z.grow[n][r] = kNoMax;
+    z.l[n] = 0;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z.o[n][j][e] = 0.0f;
+  }
+}
+
+// A page whose first place is `first` into the state; the places below `open` are seen by every row.
+template <int D, int NT>
+__device__ __forceinline__ void take_page(const uint8_t* page, int first, int open, int len, const int (&seen)[NT][2],
+                                          const uint32_t (&qf)[NT][D / 16][2], const float (&factor)[NT][2],
+                                          State<D, NT>& z) {
+  // a whole page at once, or halves where the state of two row tiles takes the registers
+  constexpr int X = NT == 1 || D == 64 ? 4 : 2;
+#pragma unroll 1
+  for (int x0 = 0; x0 < 4; x0 += X) {
+    if (first + kKv4Page <= open)
+      take<D, NT, X, false>(page, x0, first, len, seen, qf, factor, z);
+    else if (first + 16 * x0 < len)
+      take<D, NT, X, true>(page, x0, first, len, seen, qf, factor, z);
+  }
+}
+
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Args a) {
   using M = Map<D>;
@@ -487,36 +519,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Ar
     float factor[NT][2];
     load_q<T, D, NT>(a, at.s, at.kvh, at.tile * kTileRows, qf, factor);
     int seen[NT][2];  // one past the last place each of the lane's rows sees
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) seen[n][r] = open + (at.tile * kTileRows + 8 * n + 2 * c + r) / a.group;
     State<D, NT> z;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        seen[n][r] = open + (at.tile * kTileRows + 8 * n + 2 * c + r) / a.group;
-        z.m[n][r] = z.grow[n][r] = kNoMax;
-      }
-      z.l[n] = 0;
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) z.o[n][j][e] = 0.0f;
-    }
+    clear(z);
 
     bool ok = true;
     for (int k = 0; k < mine && ok; ++k) {
       ok = pr.wait(abort_v, a.status);
       if (!ok) break;
-      const uint8_t* page = ring + pr.taken % M::kStages * L::kBytes;
-      const int first = (p0 + k) * kKv4Page;
-      // a whole page at once, or halves where the state of two row tiles takes the registers
-      constexpr int X = NT == 1 || D == 64 ? 4 : 2;
-#pragma unroll 1
-      for (int x0 = 0; x0 < 4; x0 += X) {
-        if (first + kKv4Page <= open)
-          take<D, NT, X, false>(page, x0, first, len, seen, qf, factor, z);
-        else if (first + 16 * x0 < len)
-          take<D, NT, X, true>(page, x0, first, len, seen, qf, factor, z);
-      }
+      take_page<D, NT>(ring + pr.taken % M::kStages * L::kBytes, (p0 + k) * kKv4Page, open, len, seen, qf, factor, z);
       ++pr.taken;
       __syncwarp();
       if (next < mine) {
@@ -568,6 +582,155 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Ar
     }
     x += p1 - p0;
   }
+}
+
+// Few and short sequences: a cluster of eight CTAs holds a unit. Its 32 warps
+// take every 32nd page each and join their sums through distributed shared
+// memory, CTA r the rows r (and r + 8): one launch, nothing through memory.
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+template <typename T, int D, int NT>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, kCtasPerSm)
+    kv4_cluster_attn_kernel(const Args a) {
+  using M = Map<D>;
+  using L = Kv4Layout<D>;
+  constexpr int kTileRows = 8 * NT;
+  static_assert(M::kRing >= kTileRows * D * 4, "a warp's O tile fits its ring");
+  static_assert(kCluster * kWarps == 32, "a lane per warp of the cluster");
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Smem<D> sm;
+  __shared__ float2 ml[kWarps][kTileRows];
+  __shared__ float4 join[kWarps][D / 4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  uint8_t* ring = smem + warp * M::kRing;
+  PageRing<D> pr{smem_u32(ring), smem_u32(sm.bars[warp])};
+  init_smem(sm, warp, lane);
+  volatile int* abort_v = &sm.abort_flag;
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int per_seq = a.c.kv_heads * a.row_tiles, unit = blockIdx.x / kCluster;
+  const int s = unit / per_seq, kvh = unit % per_seq / a.row_tiles, tile = unit % a.row_tiles;
+  const int len = kv4_len(a.c, s, threadIdx.x == 0 ? a.status : nullptr);
+  const int pages = (len + kKv4Page - 1) / kKv4Page;
+  const int w0 = rank * kWarps + warp;
+  const int mine = (pages - w0 + 31) / 32;  // pages w0, w0 + 32, ...
+  int ids = 0;
+  auto issue = [&](int k) {  // k in order, all lanes together
+    if (k % 32 == 0) {
+      const int e = w0 + (k + lane) * 32;
+      ids = e < pages ? static_cast<int>(kv4_page(a.c, s, e, a.status)) : 0;
+    }
+    pr.issue(a.c.pages + (static_cast<int64_t>(__shfl_sync(0xffffffffu, ids, k % 32)) * a.c.kv_heads + kvh) * L::kBytes, lane);
+  };
+  int next = 0;
+  for (; next < min(mine, M::kStages); ++next) issue(next);
+
+  const int open = len - a.q_len + 1;
+  uint32_t qf[NT][M::kSteps][2];
+  float factor[NT][2];
+  load_q<T, D, NT>(a, s, kvh, tile * kTileRows, qf, factor);
+  int seen[NT][2];
+  State<D, NT> z;
+  clear(z);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) seen[n][r] = open + (tile * kTileRows + 8 * n + 2 * c + r) / a.group;
+
+  // a copy that never arrives: the status word says so, the cluster goes on to its barriers
+  for (int k = 0; k < mine; ++k) {
+    if (!pr.wait(abort_v, a.status)) break;
+    take_page<D, NT>(ring + pr.taken % M::kStages * L::kBytes, (w0 + k * 32) * kKv4Page, open, len, seen, qf, factor, z);
+    ++pr.taken;
+    __syncwarp();
+    if (next < mine) {
+      issue(next);
+      ++next;
+    }
+  }
+
+  // each warp's sums into its ring
+  float* own = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float l[2];
+    unpack2(z.l[n], l[0], l[1]);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+      const int tr = 8 * n + 2 * c + r;
+      if (g == 0) ml[warp][tr] = make_float2(z.m[n][r] == kNoMax ? -INFINITY : z.m[n][r] * factor[n][r], l[r]);
+#pragma unroll
+      for (int j = 0; j < D / 16; j += 2)
+        *reinterpret_cast<float4*>(own + tr * D + g * (D / 8) + 2 * j) =
+            make_float4(z.o[n][j][r], z.o[n][j][2 + r], z.o[n][j + 1][r], z.o[n][j + 1][2 + r]);
+    }
+  }
+  cluster_sync_all();
+  const uint32_t ml0 = smem_u32(&ml[0][0]), ring0 = smem_u32(smem);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int tr = 8 * n + rank, row = tile * kTileRows + tr;
+    if (row >= a.rows) break;  // the same in the whole CTA
+    // lane i: the part of warp i of the cluster
+    const float2 part = ld_cluster2(mapa_shared(ml0 + ((lane % kWarps) * kTileRows + tr) * 8, lane / kWarps));
+    float top = part.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float f = part.x == top ? 1.0f : ex2(part.x - top);
+    float sum = part.y * f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    // this warp's eight parts, each lane four columns
+    constexpr int kEach = 32 / kWarps;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool cols = lane * 4 < D;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int p = warp * kEach + i;
+      const float fp = __shfl_sync(0xffffffffu, f, p);
+      if (cols) {
+        const float4 u = ld_cluster4(mapa_shared(ring0 + (p % kWarps) * M::kRing + (tr * D + lane * 4) * 4, p / kWarps));
+        t.x += u.x * fp; t.y += u.y * fp; t.z += u.z * fp; t.w += u.w * fp;
+      }
+    }
+    if (cols) join[warp][lane] = t;
+    __syncthreads();
+    if (warp == 0) {
+      const float inv = sum == 0.0f ? 0.0f : a.c.v_sg / sum;
+      if (cols) {
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+          const float4 u = join[w][lane];
+          t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+        }
+        store4<T>(static_cast<T*>(a.out) +
+                      ((static_cast<int64_t>(s) * a.q_len + row / a.group) * a.heads + kvh * a.group + row % a.group) * D +
+                      lane * 4,
+                  t.x * inv, t.y * inv, t.z * inv, t.w * inv);
+      }
+      if (a.lse != nullptr && lane == 0)
+        a.lse[(static_cast<int64_t>(s) * a.c.kv_heads + kvh) * a.rows + row] = sum == 0.0f ? INFINITY : top + log2f(sum);
+    }
+    __syncthreads();
+  }
+  cluster_sync_all();  // the others may still read this CTA's sums
 }
 
 // Joins the partial sums of one row of a unit that was cut: a CTA per row, of two
@@ -783,7 +946,8 @@ bool smem_ready() {
   if (dev < 64 && done[dev]) return true;
   constexpr int most = kWarps * Map<D>::kRing + (kMaxSeqs + 1) * 4;
   if (cudaFuncSetAttribute(kv4_attn_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
-      cudaFuncSetAttribute(kv4_weights_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+      cudaFuncSetAttribute(kv4_weights_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+      cudaFuncSetAttribute(kv4_cluster_attn_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
     return false;
   if (dev < 64) done[dev] = true;
   return true;
@@ -840,7 +1004,11 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
   a.lse = weights == nullptr ? nullptr : reinterpret_cast<float*>(w + z.prefix + z.part_o + z.part_ml);
   const size_t smem = kWarps * (head_dim == 128 ? Map<128>::kRing : Map<64>::kRing) +
                       (static_cast<size_t>(z.seqs) + 1) * 4;
-  auto run = [&](auto attn, auto combine, int join_threads, auto weigh, int elem, bool ready) -> int {
+  // A small batch: every unit's cluster runs at once, and no warp has more than a few
+  // pages. One sequence of 3,242 places, 32/8 heads of 128: 12.6 us by runs, @@ by clusters.
+  const int64_t units = static_cast<int64_t>(c0.n_seqs) * c0.kv_heads * a.row_tiles;
+  const bool small = units * kCluster <= 2LL * num_sms() && c0.max_pages <= kClusterPages;
+  auto run = [&](auto attn, auto cluster, auto combine, int join_threads, auto weigh, int elem, bool ready) -> int {
     if (!ready) return VLM_ERR_CUDA;
     for (int first = 0; first < c0.n_seqs; first += kMaxSeqs) {
       a.c = c0;
@@ -852,8 +1020,9 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
       a.weights = weights == nullptr
                       ? nullptr
                       : weights + static_cast<int64_t>(first) * c0.kv_heads * c0.max_pages * kKv4Page;
-      cudaError_t e = launch_pdl(attn, dim3(grid), dim3(kThreads), smem, s, a);
-      if (e == cudaSuccess)
+      cudaError_t e = small ? launch_pdl(cluster, dim3(kCluster * units), dim3(kThreads), smem, s, a)
+                            : launch_pdl(attn, dim3(grid), dim3(kThreads), smem, s, a);
+      if (e == cudaSuccess && !small)
         e = launch_pdl(combine, dim3(a.c.n_seqs * a.c.kv_heads, a.rows), dim3(join_threads), 0, s, a);
       if (e == cudaSuccess && weights != nullptr) e = launch_pdl(weigh, dim3(grid), dim3(kThreads), smem, s, a);
       if (e != cudaSuccess) return VLM_ERR_CUDA;
@@ -865,7 +1034,7 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
     using T = decltype(type);
     constexpr int D = decltype(dim)::value, NT = decltype(nt)::value;
     const bool few = a.runs <= 12LL * z.seqs * c0.kv_heads * a.row_tiles;
-    return run(kv4_attn_kernel<T, D, NT>, few ? kv4_combine_kernel<T, D, 2> : kv4_combine_kernel<T, D, 8>, few ? 64 : 256,
+    return run(kv4_attn_kernel<T, D, NT>, kv4_cluster_attn_kernel<T, D, NT>, few ? kv4_combine_kernel<T, D, 2> : kv4_combine_kernel<T, D, 8>, few ? 64 : 256,
                kv4_weights_kernel<T, D, NT>, 2, smem_ready<T, D, NT>());
   };
   auto by_rows = [&](auto type, auto dim) {
@@ -876,7 +1045,7 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
   };
   const int rc = dtype == VLM_DTYPE_F16 ? by_dim(__half()) : by_dim(__nv_bfloat16());
   launch_end(KC_KV4_ATTN, s);
-  note_extra_launches(((c0.n_seqs + kMaxSeqs - 1) / kMaxSeqs) * (weights != nullptr ? 3 : 2) - 1);
+  note_extra_launches(((c0.n_seqs + kMaxSeqs - 1) / kMaxSeqs) * ((weights != nullptr ? 2 : 1) + (small ? 0 : 1)) - 1);
   return rc;
 }
 
