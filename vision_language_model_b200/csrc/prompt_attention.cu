@@ -29,13 +29,17 @@
 // several) have weight 0.
 // Bound, D = 128: the chain of hand-overs through the shared S buffer. S_0 is
 // copied (250 cycles), handed over (350), S_1's product runs (512) and is
-// reported (430): about 3,200 cycles per key tile against the tensor core's
+// reported (430): about 3,000 cycles per key tile against the tensor core's
 // 2,048 and the exponential unit's 1,800. Handing S over in halves of 64 keys
-// (N = 64 products) was slower. D = 64: the softmax itself, 2,700 cycles per key
+// (N = 64 products) was slower. D = 64: the softmax itself, 2,500 cycles per key
 // tile. An item costs some 5,000 cycles besides: its last product, O to memory,
-// and the look at V below. Measured, 32/8 heads of 128, bf16: 4,096 tokens 118
-// us, 1,162 TFLOP/s (0.70 of the measured peak); 8,192 tokens 434 us, 1,268;
-// heads of 64: 8,192 tokens 400 us, 690 TFLOP/s.
+// and the look at V below. Measured, 32/8 heads of 128, bf16: 4,096 tokens 112
+// to 116 us, 1,190 to 1,230 TFLOP/s (0.72 to 0.75 of the measured peak, by the box);
+// 8,192 tokens 411 to 425 us, 1,290 to 1,340;
+// heads of 64: 8,192 tokens 367 to 373 us, 740. The softmax's instructions
+// count as well, 66% of the issue slots: exponentials from polynomials beside
+// the unit (2% slower), maxima exchanged on every tile instead of where one
+// moves and a vote on the logits' size per tile (5% together) went for that.
 // TMEM, D = 128: one S buffer that the row tiles take in turn [0, 128), P
 // [128, 192) and [192, 256), O [256, 384) and [384, 512); a tile's logits leave
 // S for registers at once, so the buffer is free again while its softmax runs.
@@ -195,6 +199,16 @@ __device__ __forceinline__ bool mbar_poll_warp(uint32_t bar, uint32_t parity, vo
       if (__any_sync(0xffffffffu, stop)) return false;
     }
   }
+}
+// The 64 threads of a named barrier meet; true for all if `mine` is for one.
+__device__ __forceinline__ bool bar_any(int id, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(static_cast<uint32_t>(mine)), "r"(id)
+      : "memory");
+  return any != 0;
 }
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -455,17 +469,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int n = it.n;
       const bool idle = it.tok(t, args.tpt) >= it.q_len;  // a row tile without tokens
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f, ref = 0.0f;  // ref: m, or 0 before the row sees a key
+      bool large = false;
       for (int j = 0; j < n; ++j) {
         if (ok) ok = mbar_poll_warp(smem_u32(s_full + t), sc & 1, abort_v, args.status);
         ++sc;
         if (!ok) {
-          bar_sync(pair_id, 64);
+          if (!idle && bar_any(pair_id, false)) bar_sync(pair_id, 64);
           continue;
         }
         tc_fence_after();
         if (idle) {
-          bar_sync(pair_id, 64);
           warp_arrive(smem_u32(s_free + t), lane);
           if (j > 0) ok = mbar_wait_warp(smem_u32(o_done + t), (oc - 1) & 1, abort_v, args.status);
           if (ok) warp_arrive(smem_u32(p_full + t), lane);
@@ -483,26 +497,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < HK; ++c)
             if (c >= nvalid) u[c] = __float_as_uint(-INFINITY);
         }
-        const float m_own = row_max<true>(u);
-        xmax[((j & 1) * 2 + hf) * kRows + r] = m_own;
-        bar_sync(pair_id, 64);
-        const float m_cand = fmaxf(m_own, xmax[((j & 1) * 2 + (hf ^ 1)) * kRows + r]);
-        const bool grow = m_cand > m + grow_by;
-        const float m_new = grow ? m_cand : m;
-        const float corr = grow ? ex2((m - m_new) * args.sl2) : 1.0f;
-        const bool any_grow = __any_sync(0xffffffffu, grow);
-        m = m_new;
-        const float ref = m == -INFINITY ? 0.0f : m;
+        // The two threads of a row meet here; only where one of the 32 rows' maxima
+        // moves do they tell each other theirs.
+        const float m_own = row_max(u);
+        const bool grows = bar_any(pair_id, m_own > m + grow_by);
+        float corr = 1.0f;
+        if (grows) {
+          xmax[((j & 1) * 2 + hf) * kRows + r] = m_own;
+          bar_sync(pair_id, 64);
+          const float m_cand = fmaxf(m_own, xmax[((j & 1) * 2 + (hf ^ 1)) * kRows + r]);
+          if (m_cand > m + grow_by) {
+            corr = ex2((m - m_cand) * args.sl2);
+            m = m_cand;
+          }
+          l *= corr;
+          ref = m == -INFINITY ? 0.0f : m;
+          // Logits of ordinary size: 2^(s sl2 - m sl2) in one operation; the rounding of
+          // m sl2 scales the row's weights by up to 2^(2^-13) alike. Masked tiles and
+          // large logits are subtracted before they are scaled. (Rows without a token do
+          // not vote: they hold other sequences' queries or nothing.)
+          large = __any_sync(0xffffffffu, live && fabsf(ref * args.sl2) > 4096.0f);
+        }
         uint32_t pk[HK / 2];
-        // Logits of ordinary size: 2^(s sl2 - m sl2) in one operation; the rounding of
-        // m sl2 scales the row's weights by up to 2^(2^-13) alike. Masked tiles and large
-        // logits: subtracted before they are scaled, and no polynomial.
-        // (Rows without a token do not vote: they hold other sequences' queries or nothing.)
-        const bool plain = !masked && !__any_sync(0xffffffffu, live && fabsf(ref * args.sl2) > 4096.0f);
-        const float sum = plain ? row_exp<true, kHalf>(u, sl2x2, ref * args.sl2, pk)
-                                : row_exp<false, kHalf, true>(u, sl2x2, ref, pk);
-        l = l * corr + sum;
-        if (!(m_own < INFINITY)) l = NAN;  // a NaN or infinite logit: exp2_poly would swallow it
+        l += !masked && !large ? row_exp<false, kHalf>(u, sl2x2, ref * args.sl2, pk)
+                               : row_exp<false, kHalf, true>(u, sl2x2, ref, pk);
         if (j > 0) {
           // the product with the tile before must be done before O is rescaled and P overwritten
           ok = mbar_wait_warp(smem_u32(o_done + t), (oc - 1) & 1, abort_v, args.status);
@@ -510,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
         }
         tmem_st32(trow + C::p_col(t) + 32 * hf, pk);
-        if (j > 0 && any_grow) {
+        if (j > 0 && grows) {
 #pragma unroll
           for (int x = 0; x < D / 64; ++x) {
             const uint32_t col = trow + C::o_col(t) + (D / 2) * hf + 32 * x;

@@ -45,15 +45,8 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-__device__ __forceinline__ float max3f_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// Row maximum of N values with four independent chains of 3-input max. kNan:
-// a NaN among them is the result, else it is passed over.
-template <bool kNan = false, int N>
+// Row maximum of N values with four independent chains of 3-input max.
+template <int N>
 __device__ __forceinline__ float row_max(const uint32_t (&u)[N]) {
   constexpr int NC = 4;
   float m[NC];
@@ -64,13 +57,13 @@ __device__ __forceinline__ float row_max(const uint32_t (&u)[N]) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const float x = __uint_as_float(u[c + 2 * i]), y = __uint_as_float(u[c + 2 * i + 1]);
-      m[i] = kNan ? max3f_nan(m[i], x, y) : max3f(m[i], x, y);
+      m[i] = max3f(m[i], x, y);
     }
   }
 #pragma unroll
   for (int w = NC / 2; w > 0; w /= 2)
 #pragma unroll
-    for (int i = 0; i < w; ++i) m[i] = kNan ? max3f_nan(m[i], m[i + w], m[i + w]) : fmaxf(m[i], m[i + w]);
+    for (int i = 0; i < w; ++i) m[i] = fmaxf(m[i], m[i + w]);
   return m[0];
 }
 
