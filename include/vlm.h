@@ -429,8 +429,9 @@ VLM_API int vlm_expand_placeholders(const int64_t* d_input_ids, int64_t n_ids, i
  *   listed queries are written. Keys and values that a row does not see do not
  *   reach it, infinities and NaN included; a NaN logit makes its row NaN.
  *   scale > 0. P is rounded to dtype, sums are fp32. A sequence's rows do not
- *   depend on the other sequences. No workspace. d_status may be NULL here and
- *   in the vlm_kv4_* calls (device-side errors then go unreported).
+ *   depend on the other sequences. No workspace; d_out must not overlap k and
+ *   v. d_status may be NULL here and in the vlm_kv4_* calls (device-side errors
+ *   then go unreported).
  * ------------------------------------------------------------------------- */
 VLM_API int vlm_prompt_attention(int dtype, int heads, int kv_heads, int head_dim, const int32_t* q_lens,
                                  const int32_t* kv_lens, int n_seqs, const void* d_q, int64_t q_stride,
@@ -458,7 +459,7 @@ VLM_API int vlm_prompt_attention(int dtype, int heads, int kv_heads, int head_di
  *   *d_status = VLM_ERR_BAD_PAGE; nothing outside the pool is touched, the
  *   outputs of the sequences concerned are unspecified (written and read rows
  *   without a page are skipped).
- * n_seqs <= 65535.
+ * n_seqs <= 65535; max_pages <= 33554303, so that places keep within 32 bits.
  *
  * vlm_kv4_append: quantises new rows k, v (16-bit, strided) into the places
  *   from d_lens[s] on (d_lens: tokens in the cache before; NULL: 0). Sequence

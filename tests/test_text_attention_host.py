@@ -164,3 +164,12 @@ def test_binding_refuses_tensors_off_the_gpu_and_of_other_shapes():
         vlm.kv4_append(pages[:, :, :70], torch.zeros((1, 2), dtype=torch.int32), None, q, q, 1.0, 1.0)
     with pytest.raises(TypeError):
         vlm._dtype16(torch.float32)
+
+
+@pytest.mark.parametrize("call", [_append, _read, _attend, _evict])
+def test_tables_whose_places_leave_no_room_in_32_bits_are_refused(L, call):
+    # the kernels step over places by up to 4,096, so a table may not reach to the end of 32 bits
+    room = (2 ** 31 - 1 - 8192) // 64
+    assert call(L, width=room + 1, n=1) == vlm.ERR_BAD_SHAPE
+    if call is _evict:
+        assert _evict(L, to_width=room + 1, n=1) == vlm.ERR_BAD_SHAPE
