@@ -164,6 +164,14 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// For a copy that the CTA's end must wait for, whoever has given up: until it has
+// landed, for kWaitBudgetCycles at most.
+__device__ __forceinline__ void mbar_wait_landed(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity) && clock64() - t0 <= kWaitBudgetCycles) {
+  }
+}
+
 // mbar_wait for all 32 lanes of a warp with one shared result, so the warp-wide
 // (.sync.aligned) tcgen05 instructions that follow never diverge.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort,

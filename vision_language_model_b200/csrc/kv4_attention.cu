@@ -215,6 +215,13 @@ struct PageRing {
     constexpr uint32_t n = Map<D>::kStages;
     return mbar_wait_warp(bars + taken % n * 8, (taken / n) & 1, abort, status);
   }
+  // After a wait gave up: the copies still under way land, or are given up as well,
+  // before the warp puts the ring to other use or ends.
+  __device__ __forceinline__ void drain() {
+    constexpr uint32_t n = Map<D>::kStages;
+    for (; taken != issued; ++taken) mbar_wait_landed(bars + taken % n * 8, (taken / n) & 1);
+    __syncwarp();
+  }
 };
 
 // S^T = (code * scale) . q for tokens [16 x0, 16 (x0 + X)) of a page in shared
@@ -491,7 +498,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Ar
   for (int s = blockIdx.x; s < a.c.n_seqs; s += gridDim.x) {
     if (prefix[s + 1] != prefix[s]) continue;
     uint2* dst = reinterpret_cast<uint2*>(static_cast<T*>(a.out) + static_cast<int64_t>(s) * a.q_len * a.heads * D);
-    for (int i = threadIdx.x; i < a.q_len * a.heads * D / 4; i += kThreads) dst[i] = make_uint2(0, 0);
+    const int64_t n = static_cast<int64_t>(a.q_len) * a.heads * (D / 4);
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) dst[i] = make_uint2(0, 0);
   }
 
   // runs go to CTAs in turn, so that few runs spread over the SMs
@@ -538,7 +546,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Ar
         ++next;
       }
     }
-    if (!ok) break;  // a copy that never arrived: the status word says so
+    if (!ok) {  // a copy that never arrived: the status word says so
+      pr.drain();
+      break;
+    }
 
     // the rows' results, or partial sums where the unit goes on in other runs
     const bool whole = p0 == 0 && p1 == at.pages;
@@ -663,6 +674,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, kCt
       ++next;
     }
   }
+  pr.drain();
 
   // each warp's sums into its ring
   float* own = reinterpret_cast<float*>(ring);
@@ -929,7 +941,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_weights_kernel(const
         ++next;
       }
     }
-    if (!ok) break;
+    if (!ok) {
+      pr.drain();
+      break;
+    }
     x += p1 - p0;
   }
 }

@@ -371,6 +371,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      // Every copy has landed, or is given up, before the CTA ends: as a rule the products
+      // wait for it anyway, after an abort nobody else does.
+      if (qc > 0) mbar_wait_landed(smem_u32(q_full), (qc - 1) & 1);
+      for (uint32_t st = 0; st < kStages; ++st) {
+        // fills of stage st so far: its last one is in phase (fills - 1)
+        const uint32_t kf = (kc + kStages - 1 - st) / kStages, vf = (vc + kStages - 1 - st) / kStages;
+        if (kf > 0) mbar_wait_landed(smem_u32(k_full + st), (kf - 1) & 1);
+        if (vf > 0) mbar_wait_landed(smem_u32(v_full + st), (vf - 1) & 1);
+      }
     }
   } else if (warp < 3) {
     // The whole warp walks the loop and one elected lane issues: descriptors
