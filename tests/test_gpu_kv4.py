@@ -136,7 +136,9 @@ def _attend_width(lens, heads, kv_heads, dim, q_len, dtype, seed, weights, gain,
     ([4000], 2, 1, 128, 1),
     ([8192, 1], 16, 1, 64, 1),   # as many pages as a small batch may have
     ([100] * 9, 8, 4, 64, 1),
-    ([100] * 10, 8, 4, 64, 1),   # one unit more than clusters take on a GPU of 148 SMs
+    ([100] * 10, 8, 4, 64, 1),
+    ([100] * 55, 2, 1, 64, 1),   # as many units as clusters take on a GPU of 148 SMs
+    ([100] * 56, 2, 1, 64, 1),   # and one more
 ])
 def test_attention_over_the_cache(lens, heads, kv_heads, dim, q_len, dtype):
     _attend(lens, heads, kv_heads, dim, q_len, dtype, weights=False)
@@ -149,6 +151,18 @@ def test_attention_over_the_cache(lens, heads, kv_heads, dim, q_len, dtype):
     ([1500], 20, 2, 128, 5, torch.float16),
 ])
 def test_attention_sums_each_places_weight(lens, heads, kv_heads, dim, q_len, dtype):
+    _attend(lens, heads, kv_heads, dim, q_len, dtype, weights=True)
+
+
+@pytest.mark.parametrize("lens,heads,kv_heads,dim,q_len,dtype", [
+    ([8192, 4100, 1], 16, 1, 128, 1, torch.bfloat16),   # four pages per warp, a ring of two
+    ([2049, 0, 5, 6000], 16, 4, 128, 4, torch.float16),  # two tiles of rows side by side
+    ([8192, 2047], 4, 1, 64, 3, torch.float16),
+    ([3000, 700], 40, 1, 128, 3, torch.bfloat16),       # several row tiles: weights in a launch of their own
+    ([2100] + [65] * 26, 8, 4, 64, 1, torch.bfloat16),  # 108 units: two waves of clusters
+    ([2100] + [65] * 27, 8, 4, 64, 1, torch.bfloat16),  # 112: by runs
+])
+def test_weights_from_the_cluster_that_attends(lens, heads, kv_heads, dim, q_len, dtype):
     _attend(lens, heads, kv_heads, dim, q_len, dtype, weights=True)
 
 

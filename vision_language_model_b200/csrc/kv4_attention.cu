@@ -595,15 +595,78 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Ar
   }
 }
 
+// The two of a page's 64 places that a lane adds to: tokens g and g + 8 (by c & 1) of
+// tiles c >> 1 and 2 + (c >> 1).
+template <int D>
+__device__ __forceinline__ int own_place(int first, int h) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  return first + 32 * h + 16 * (c >> 1) + Map<D>::token(c & 1, g >> 1, g & 1);
+}
+template <int D>
+__device__ __forceinline__ void weights_before(const float* dst, int first, int len, float (&before)[2]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) before[h] = own_place<D>(first, h) < len ? dst[own_place<D>(first, h)] : 0.0f;
+}
+
+// dst[j] = before + the sum over the rows of 2^(logit - norm) for the places of a page:
+// the logits once more from its keys. rows_of(tile) sets the rows of a row tile, where
+// there are several.
+template <int D, int NT, typename Rows>
+__device__ __forceinline__ void weigh_page(const uint8_t* page, int first, int len, int row_tiles, Rows rows_of,
+                                           const uint32_t (&qf)[NT][D / 16][2], const float (&factor)[NT][2],
+                                           const float (&norm)[NT][2], const int (&seen)[NT][2],
+                                           const float (&before)[2], float* dst) {
+  using M = Map<D>;
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (first + 32 * h >= len) continue;
+    float w[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // tokens g and g + 8 of both tiles
+    for (int tile = 0; tile < row_tiles; ++tile) {
+      if (row_tiles > 1) rows_of(tile);
+      float s[2][NT][4];
+      logits<D, NT, 2>(page, 2 * h, qf, s);
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = first + 32 * h + 16 * y + M::token(e >> 1, g >> 1, g & 1);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float p2 = ex2(__fmul_rn(s[y][n][e], factor[n][e & 1]) - norm[n][e & 1]);
+            w[y][e >> 1] += j < seen[n][e & 1] ? p2 : 0.0f;
+          }
+        }
+    }
+    float own = 0.0f;
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float v = w[y][i];
+        v += __shfl_xor_sync(0xffffffffu, v, 1);
+        v += __shfl_xor_sync(0xffffffffu, v, 2);
+        if (c == 2 * y + i) own = v;
+      }
+    if (own_place<D>(first, h) < len) dst[own_place<D>(first, h)] = before[h] + own;
+  }
+}
+
 // Few and short sequences: a cluster of eight CTAs holds a unit. Its 32 warps
 // take every 32nd page each and join their sums through distributed shared
-// memory, CTA r the rows r (and r + 8): one launch, nothing through memory.
+// memory, CTA r the rows r (and r + 8): one launch, nothing through memory. Weights,
+// where they are wanted and one row tile holds the unit, follow in the same launch.
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "r"(addr)
                : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_cluster1(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
@@ -618,11 +681,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, kCt
   using M = Map<D>;
   using L = Kv4Layout<D>;
   constexpr int kTileRows = 8 * NT;
-  static_assert(M::kRing >= kTileRows * D * 4, "a warp's O tile fits its ring");
+  static_assert(L::kBytes >= kTileRows * D * 4, "a warp's O tile fits a stage of its ring");
   static_assert(kCluster * kWarps == 32, "a lane per warp of the cluster");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Smem<D> sm;
   __shared__ float2 ml[kWarps][kTileRows];
+  __shared__ uint32_t sums_at[kWarps];
   __shared__ float4 join[kWarps][D / 4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   uint8_t* ring = smem + warp * M::kRing;
@@ -676,8 +740,15 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, kCt
   }
   pr.drain();
 
-  // each warp's sums into its ring
-  float* own = reinterpret_cast<float*>(ring);
+  // each warp's sums into the last stage that it read; the stages before it take the
+  // first pages again where the weights are wanted
+  const bool weigh = a.weights != nullptr && a.row_tiles == 1;
+  const uint32_t last = (pr.issued + M::kStages - 1) % M::kStages * L::kBytes;
+  if (lane == 0) sums_at[warp] = last;
+  float* own = reinterpret_cast<float*>(ring + last);
+  next = 0;
+  if (weigh)
+    for (; next < min(mine, M::kStages - 1); ++next) issue(next);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     float l[2];
@@ -696,6 +767,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, kCt
   }
   cluster_sync_all();
   const uint32_t ml0 = smem_u32(&ml[0][0]), ring0 = smem_u32(smem);
+  // lane i: where warp i of the cluster left its sums
+  const uint32_t part_at = mapa_shared(ring0 + lane % kWarps * M::kRing, lane / kWarps) +
+                           ld_cluster1(mapa_shared(smem_u32(&sums_at[lane % kWarps]), lane / kWarps));
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int tr = 8 * n + rank, row = tile * kTileRows + tr;
@@ -717,8 +791,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, kCt
     for (int i = 0; i < kEach; ++i) {
       const int p = warp * kEach + i;
       const float fp = __shfl_sync(0xffffffffu, f, p);
+      const uint32_t from = __shfl_sync(0xffffffffu, part_at, p);
       if (cols) {
-        const float4 u = ld_cluster4(mapa_shared(ring0 + (p % kWarps) * M::kRing + (tr * D + lane * 4) * 4, p / kWarps));
+        const float4 u = ld_cluster4(from + (tr * D + lane * 4) * 4);
         t.x += u.x * fp; t.y += u.y * fp; t.z += u.z * fp; t.w += u.w * fp;
       }
     }
@@ -742,7 +817,33 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, kCt
     }
     __syncthreads();
   }
-  cluster_sync_all();  // the others may still read this CTA's sums
+  cluster_sync_all();  // the others have read this CTA's sums, and every row's lse is written
+  if (!weigh) return;
+  fence_proxy_async_smem();
+  float norm[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = 8 * n + 2 * c + r;
+      norm[n][r] = row < a.rows ? a.lse[(static_cast<int64_t>(s) * a.c.kv_heads + kvh) * a.rows + row] : INFINITY;
+      if (row >= a.rows) seen[n][r] = 0;
+    }
+  float* dst = a.weights + (static_cast<int64_t>(s) * a.c.kv_heads + kvh) * a.c.max_pages * kKv4Page;
+  for (int k = 0; k < mine; ++k) {
+    if (next < mine) {
+      issue(next);
+      ++next;
+    }
+    const int first = (w0 + k * 32) * kKv4Page;
+    float before[2];
+    weights_before<D>(dst, first, len, before);
+    if (!pr.wait(abort_v, a.status)) break;
+    weigh_page<D, NT>(ring + pr.taken % M::kStages * L::kBytes, first, len, 1, [](int) {}, qf, factor, norm, seen, before, dst);
+    ++pr.taken;
+    __syncwarp();
+  }
+  pr.drain();
 }
 
 // Joins the partial sums of one row of a unit that was cut: a CTA per row, of two
@@ -845,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_weights_kernel(const
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Smem<D> sm;
   int* prefix = reinterpret_cast<int*>(smem + kWarps * M::kRing);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 3;
   const uint8_t* ring = smem + warp * M::kRing;
   PageRing<D> pr{smem_u32(ring), smem_u32(sm.bars[warp])};
   init_smem(sm, warp, lane);
@@ -890,50 +991,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_weights_kernel(const
     rows_of(0);
     bool ok = true;
     for (int k = 0; k < mine; ++k) {
-      // each lane adds to two of the 64 places: tokens g and g + 8 (by c & 1) of tiles c >> 1 and 2 + (c >> 1)
       const int first = (p0 + k) * kKv4Page;
-      int j_own[2];
       float before[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        j_own[h] = first + 32 * h + 16 * (c >> 1) + M::token(c & 1, g >> 1, g & 1);
-        before[h] = j_own[h] < len ? dst[j_own[h]] : 0.0f;
-      }
+      weights_before<D>(dst, first, len, before);
       ok = pr.wait(abort_v, a.status);
       if (!ok) break;
-      const uint8_t* page = ring + pr.taken % M::kStages * L::kBytes;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (first + 32 * h >= len) continue;
-        float w[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // tokens g and g + 8 of both tiles
-        for (int tile = 0; tile < a.row_tiles; ++tile) {
-          if (a.row_tiles > 1) rows_of(tile);
-          float s[2][NT][4];
-          logits<D, NT, 2>(page, 2 * h, qf, s);
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = first + 32 * h + 16 * y + M::token(e >> 1, g >> 1, g & 1);
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                const float p2 = ex2(__fmul_rn(s[y][n][e], factor[n][e & 1]) - norm[n][e & 1]);
-                w[y][e >> 1] += j < seen[n][e & 1] ? p2 : 0.0f;
-              }
-            }
-        }
-        float own = 0.0f;
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float v = w[y][i];
-            v += __shfl_xor_sync(0xffffffffu, v, 1);
-            v += __shfl_xor_sync(0xffffffffu, v, 2);
-            if (c == 2 * y + i) own = v;
-          }
-        if (j_own[h] < len) dst[j_own[h]] = before[h] + own;
-      }
+      weigh_page<D, NT>(ring + pr.taken % M::kStages * L::kBytes, first, len, a.row_tiles, rows_of, qf, factor, norm,
+                        seen, before, dst);
       ++pr.taken;
       __syncwarp();
       if (next < mine) {
@@ -1019,11 +1083,20 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
   a.lse = weights == nullptr ? nullptr : reinterpret_cast<float*>(w + z.prefix + z.part_o + z.part_ml);
   const size_t smem = kWarps * (head_dim == 128 ? Map<128>::kRing : Map<64>::kRing) +
                       (static_cast<size_t>(z.seqs) + 1) * 4;
-  // A small batch: every unit's cluster runs at once, and no warp has more than a few
-  // pages. 32/8 heads of 128, one sequence of 3,242 places: 12.6 us by runs, 8.5 by
-  // clusters; eight of 8,000, over the border: 23.2 by runs, 26.3 by clusters.
+  // A small batch goes by clusters, no warp with more than a few pages: where all units'
+  // clusters run at once, or in two waves if the weights are wanted too, which the cluster
+  // takes from the pages that it has at hand (one row tile), and the table has a page for
+  // every warp. By runs against by clusters, heads of 128, group 4: one sequence of 3,242
+  // places, 8 key heads, 12.6 and 8.5 us; 12 of up to 4,000, 4 key heads (48 units), 18.5
+  // and 12.4; 8 of up to 8,000, 8 key heads (64 units), 22.7 and 24.8. With weights, 4
+  // tokens: 24 of up to 4,000, 4 key heads (96 units), 50.8 and 45.2; of 500 places, 26.7
+  // and 33.3; heads of 64, 24 of up to 6,000, 43 and 33.
   const int64_t units = static_cast<int64_t>(c0.n_seqs) * c0.kv_heads * a.row_tiles;
-  const bool small = units * kCluster <= 2LL * num_sms() && c0.max_pages <= kClusterPages;
+  const bool fused = weights != nullptr && a.row_tiles == 1 && c0.max_pages >= kCluster * kWarps;
+  const int64_t most = static_cast<int64_t>(kCtasPerSm) * num_sms() * (fused ? 2 : 1);
+  const bool small = units * kCluster <= most && c0.max_pages <= kClusterPages;
+  const bool weigh_after = weights != nullptr && !(small && a.row_tiles == 1);
+  const int launches = 1 + (small ? 0 : 1) + (weigh_after ? 1 : 0);
   auto run = [&](auto attn, auto cluster, auto combine, int join_threads, auto weigh, int elem, bool ready) -> int {
     if (!ready) return VLM_ERR_CUDA;
     for (int first = 0; first < c0.n_seqs; first += kMaxSeqs) {
@@ -1040,7 +1113,7 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
                             : launch_pdl(attn, dim3(grid), dim3(kThreads), smem, s, a);
       if (e == cudaSuccess && !small)
         e = launch_pdl(combine, dim3(a.c.n_seqs * a.c.kv_heads, a.rows), dim3(join_threads), 0, s, a);
-      if (e == cudaSuccess && weights != nullptr) e = launch_pdl(weigh, dim3(grid), dim3(kThreads), smem, s, a);
+      if (e == cudaSuccess && weigh_after) e = launch_pdl(weigh, dim3(grid), dim3(kThreads), smem, s, a);
       if (e != cudaSuccess) return VLM_ERR_CUDA;
     }
     return VLM_OK;
@@ -1061,7 +1134,7 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
   };
   const int rc = dtype == VLM_DTYPE_F16 ? by_dim(__half()) : by_dim(__nv_bfloat16());
   launch_end(KC_KV4_ATTN, s);
-  note_extra_launches(((c0.n_seqs + kMaxSeqs - 1) / kMaxSeqs) * ((weights != nullptr ? 2 : 1) + (small ? 0 : 1)) - 1);
+  note_extra_launches(((c0.n_seqs + kMaxSeqs - 1) / kMaxSeqs) * launches - 1);
   return rc;
 }
 
