@@ -94,7 +94,7 @@ def test_append_infinities_saturate_and_nan_is_bounded():
 def _attend(lens, heads, kv_heads, dim, q_len, dtype, seed=11, weights=False, gain=1.0):
     """By clusters where the batch is small, and by runs of pages, which a table of more than 128 pages asks for."""
     _attend_width(lens, heads, kv_heads, dim, q_len, dtype, seed, weights, gain, None)
-    _attend_width(lens, heads, kv_heads, dim, q_len, dtype, seed, weights, gain, 130)
+    _attend_width(lens, heads, kv_heads, dim, q_len, dtype, seed, weights, gain, max(130, -(-max(lens) // PAGE)))
 
 
 def _attend_width(lens, heads, kv_heads, dim, q_len, dtype, seed, weights, gain, width):
@@ -139,6 +139,8 @@ def _attend_width(lens, heads, kv_heads, dim, q_len, dtype, seed, weights, gain,
     ([100] * 10, 8, 4, 64, 1),
     ([100] * 55, 2, 1, 64, 1),   # as many units as clusters take on a GPU of 148 SMs
     ([100] * 56, 2, 1, 64, 1),   # and one more
+    ([1] * 300 + [2000], 4, 2, 64, 1),   # runs of many units' starts
+    ([20000, 40, 0, 1], 8, 8, 64, 1),    # runs that end where a unit starts, before its first page
 ])
 def test_attention_over_the_cache(lens, heads, kv_heads, dim, q_len, dtype):
     _attend(lens, heads, kv_heads, dim, q_len, dtype, weights=False)

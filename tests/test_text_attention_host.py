@@ -173,3 +173,5 @@ def test_tables_whose_places_leave_no_room_in_32_bits_are_refused(L, call):
     assert call(L, width=room + 1, n=1) == vlm.ERR_BAD_SHAPE
     if call is _evict:
         assert _evict(L, to_width=room + 1, n=1) == vlm.ERR_BAD_SHAPE
+    # as many entries in all as 32-bit offsets of the sequences take, two more each
+    assert call(L, width=(2 ** 31 - 1) // 64, n=64) == vlm.ERR_BAD_SHAPE

@@ -26,17 +26,19 @@
 //     log2(e) are one fp32 factor of the logit.
 //   - P is rounded to fp16 for the second product (half a step, 2^-11); the
 //     sum of a row's weights, its maximum and both products' sums stay in fp32.
-//   - Work is cut into equal runs of pages, one per warp, over the flattened (sequence, key
-//     head, row tile, page) list, whatever the lengths, computed on the device
-//     from the lengths there, so a captured graph replays with other lengths.
+//   - Work is cut into equal runs of pages, one per warp, over the flattened
+//     (sequence, key head, row tile, page) list, whatever the lengths (a unit's
+//     start counts as two pages more), computed on the device from the lengths
+//     there, so a captured graph replays with other lengths.
 //     A unit (sequence, key head, row tile) cut by a border leaves partial sums
 //     that kv4_combine_kernel joins in the order of the runs: the result does
 //     not depend on timing (its last bits do on where the batch was cut).
-// Measured, 32/8 heads of 128: 31 sequences of up to 16,000 tokens (378 MB) 78
-// us, of which the first kernel alone 74, 5.1 TB/s (0.78 of the copy rate); what
-// it lacks is issue slots, 58% used, 430 instructions per 32 tokens of a head of
-// which 256 convert and scale. As 16-row tiles of S and O it took 104 us, with
-// fp32 logits stored for the weights they would cost 8 bytes per row and token.
+// Measured, 32/8 heads of 128: 31 sequences of up to 16,000 tokens (378 MB) 76 us,
+// of which the join is 4 to 5; three of 131,072 (452 MB) 85 us, 5.3 TB/s (0.81 of
+// the copy rate). What it lacks is issue slots, 58% used, 430 instructions per 32
+// tokens of a head of which 256 convert and scale. As 16-row tiles of S and O it
+// took 104 us. For the weights, logits stored in fp32 would cost 8 bytes per row
+// and token; they are made again from the keys.
 // Places behind what a row sees get logit -inf; value scales of places behind
 // the sequence's end are taken as 0, so stale bytes (NaN scales among them)
 // reach no sum. A row that sees nothing is 0.
@@ -58,6 +60,7 @@ constexpr int kCtasPerSm = 3;  // 168 registers; four CTAs would have to spill
 constexpr int kCluster = 8;       // CTAs that share a unit of a small batch
 constexpr int kClusterPages = 128;  // and the pages a sequence may then have: four per warp
 constexpr int kMinPages = 1;  // of a run: a page takes a warp about 1 us, joining a run less
+constexpr int kUnitPages = 2;  // pages that starting a unit counts as where the work is cut
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNoMax = -3.0e38f;  // a row's maximum before it sees a place; finite, so that -inf minus it is no NaN
 constexpr float kRescale = 8.0f;  // log2 units; P stays below 2^8
@@ -87,7 +90,7 @@ struct Args {
   int heads, group, q_len, rows, tile_rows, row_tiles;
   float scale;
   void* out;         // [n_seqs * q_len, heads, D]
-  int32_t* prefix;   // [n_seqs + 1] page offsets, written by the first kernel's CTA 0
+  int32_t* prefix;   // [n_seqs + 1] sequences' offsets in the cut, written by the first kernel's CTA 0
   float* part_o;     // [2 * runs][tile_rows][D]
   float2* part_ml;   // [2 * runs][tile_rows] maximum (log2 units) and sum
   float* lse;        // [n_seqs, kv_heads, rows] log2 of a row's sum (null: not wanted)
@@ -118,13 +121,22 @@ struct Plan {
   int64_t total, chunk;
 };
 
-// The page offsets of all sequences into shared memory (prefix[n_seqs + 1]) and the cut.
+// A unit's length in the cut: its pages behind kUnitPages without work, which stand for
+// what it costs to start one. (Without them the warp that got a short sequence's eight
+// units, two pages each, finished last: 131,072, 131,071, 77 and 98,304 places 104 us, with
+// one page 87, with two 80, with three 80; 31 ragged sequences 79, 77, 76, 76.)
+__device__ __forceinline__ int cut_length(int len) {
+  return len == 0 ? 0 : (len + kKv4Page - 1) / kKv4Page + kUnitPages;
+}
+
+// The sequences' offsets into shared memory (prefix[n_seqs + 1], units_per_seq to be
+// multiplied) and the cut.
 __device__ __forceinline__ Plan make_plan(const Kv4& c, int units_per_seq, int runs, int* prefix, int* warp_sum,
                                           int32_t* status) {
   const int n = c.n_seqs, per = (n + kThreads - 1) / kThreads;
   const int lo = min(n, static_cast<int>(threadIdx.x) * per), hi = min(n, lo + per);
   int sum = 0;
-  for (int s = lo; s < hi; ++s) sum += (kv4_len(c, s, status) + kKv4Page - 1) / kKv4Page;
+  for (int s = lo; s < hi; ++s) sum += cut_length(kv4_len(c, s, status));
   int inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -137,7 +149,7 @@ __device__ __forceinline__ Plan make_plan(const Kv4& c, int units_per_seq, int r
   for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) base += warp_sum[w];
   for (int s = lo; s < hi; ++s) {
     prefix[s] = base;
-    base += (kv4_len(c, s, nullptr) + kKv4Page - 1) / kKv4Page;
+    base += cut_length(kv4_len(c, s, nullptr));
   }
   if (hi == n && lo < n) prefix[n] = base;
   __syncthreads();
@@ -275,11 +287,15 @@ __device__ __forceinline__ void logits(const uint8_t* page, int x0, const uint32
   }
 }
 
-// Where run position x lies: sequence, key head, row tile, first page.
+// The part of a run from position x on that lies in one unit: sequence, key head, row
+// tile, the pages [p0, p1) of `pages` (none where it ends before the first), its length
+// in the cut.
 struct Place {
-  int s, kvh, tile, page, pages;
+  int s, kvh, tile, p0, p1, pages;
+  int64_t length;
 };
-__device__ __forceinline__ Place place_of(const int* prefix, int n_seqs, int kv_heads, int row_tiles, int64_t x) {
+__device__ __forceinline__ Place place_of(const int* prefix, int n_seqs, int kv_heads, int row_tiles, int64_t x,
+                                          int64_t end) {
   const int per_seq = kv_heads * row_tiles;
   int lo = 0, hi = n_seqs - 1;
   while (lo < hi) {
@@ -288,11 +304,15 @@ __device__ __forceinline__ Place place_of(const int* prefix, int n_seqs, int kv_
   }
   Place p;
   p.s = lo;
-  p.pages = prefix[lo + 1] - prefix[lo];
+  const int span = prefix[lo + 1] - prefix[lo];
+  p.pages = span - kUnitPages;
   const int64_t r = x - static_cast<int64_t>(prefix[lo]) * per_seq;
-  const int unit = r < 0x80000000LL ? static_cast<int>(static_cast<uint32_t>(r) / static_cast<uint32_t>(p.pages))
-                                    : static_cast<int>(r / p.pages);
-  p.page = static_cast<int>(r - static_cast<int64_t>(unit) * p.pages);
+  const int unit = r < 0x80000000LL ? static_cast<int>(static_cast<uint32_t>(r) / static_cast<uint32_t>(span))
+                                    : static_cast<int>(r / span);
+  const int at = static_cast<int>(r - static_cast<int64_t>(unit) * span);
+  p.length = min(static_cast<int64_t>(span - at), end - x);
+  p.p0 = max(0, at - kUnitPages);
+  p.p1 = max(0, at + static_cast<int>(p.length) - kUnitPages);
   p.kvh = unit / row_tiles;
   p.tile = unit % row_tiles;
   return p;
@@ -506,10 +526,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Ar
   const int run = warp * gridDim.x + blockIdx.x;
   const int64_t begin = run * plan.chunk;
   const int64_t end = min(plan.total, begin + plan.chunk);
-  for (int64_t x = begin; x < end;) {
-    const Place at = place_of(prefix, a.c.n_seqs, a.c.kv_heads, a.row_tiles, x);
-    const int p0 = at.page;
-    const int p1 = static_cast<int>(min(static_cast<int64_t>(at.pages), p0 + (end - x)));
+  int64_t x = begin;
+  while (x < end) {
+    const Place at = place_of(prefix, a.c.n_seqs, a.c.kv_heads, a.row_tiles, x, end);
+    const int64_t from = x;
+    x += at.length;
+    const int p0 = at.p0, p1 = at.p1;
+    if (p0 == p1) continue;
     const int len = kv4_len(a.c, at.s, nullptr);
     const int mine = p1 - p0;
     int ids = 0;  // the numbers of the next 32 pages, one per lane
@@ -553,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Ar
 
     // the rows' results, or partial sums where the unit goes on in other runs
     const bool whole = p0 == 0 && p1 == at.pages;
-    const int64_t slot = 2 * static_cast<int64_t>(run) + (x == begin ? 0 : 1);
+    const int64_t slot = 2 * static_cast<int64_t>(run) + (from == begin ? 0 : 1);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float l[2];
@@ -591,7 +614,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Ar
         }
       }
     }
-    x += p1 - p0;
   }
 }
 
@@ -864,11 +886,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_combine_kernel(const Args
   const int per_seq = a.c.kv_heads * a.row_tiles;
   const int64_t total = static_cast<int64_t>(a.prefix[a.c.n_seqs]) * per_seq;
   const int64_t chunk = max(static_cast<int64_t>(kMinPages), (total + a.runs - 1) / a.runs);
-  const int pages = a.prefix[s + 1] - a.prefix[s];
-  const int64_t lo = static_cast<int64_t>(a.prefix[s]) * per_seq + static_cast<int64_t>(kvh * a.row_tiles + tile) * pages;
-  const int i0 = static_cast<int>(lo / chunk), i1 = static_cast<int>((lo + pages - 1) / chunk);
+  const int span = a.prefix[s + 1] - a.prefix[s];
+  const int64_t lo = static_cast<int64_t>(a.prefix[s]) * per_seq + static_cast<int64_t>(kvh * a.row_tiles + tile) * span;
+  const int i0 = static_cast<int>((lo + kUnitPages) / chunk), i1 = static_cast<int>((lo + span - 1) / chunk);
   float* lse = a.lse == nullptr ? nullptr : a.lse + (static_cast<int64_t>(s) * a.c.kv_heads + kvh) * a.rows + row;
-  if (pages == 0) {
+  if (span == 0) {
     if (lse != nullptr && threadIdx.x == 0) *lse = INFINITY;
     return;
   }
@@ -957,10 +979,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_weights_kernel(const
   const int run = warp * gridDim.x + blockIdx.x;
   const int64_t begin = run * plan.chunk;
   const int64_t end = min(plan.total, begin + plan.chunk);
-  for (int64_t x = begin; x < end;) {
-    const Place at = place_of(prefix, a.c.n_seqs, a.c.kv_heads, 1, x);
-    const int p0 = at.page;
-    const int p1 = static_cast<int>(min(static_cast<int64_t>(at.pages), p0 + (end - x)));
+  int64_t x = begin;
+  while (x < end) {
+    const Place at = place_of(prefix, a.c.n_seqs, a.c.kv_heads, 1, x, end);
+    x += at.length;
+    const int p0 = at.p0, p1 = at.p1;
+    if (p0 == p1) continue;
     const int len = kv4_len(a.c, at.s, nullptr);
     const int mine = p1 - p0;
     int ids = 0;  // the numbers of the next 32 pages, one per lane
@@ -1009,7 +1033,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_weights_kernel(const
       pr.drain();
       break;
     }
-    x += p1 - p0;
   }
 }
 

@@ -43,6 +43,7 @@ int check_rows(int dtype, const void* p, int64_t stride, int64_t width) {
 // Entries of a page table: places are 32-bit in the kernels, which step over them by up
 // to 4,096 at a time, so the last place keeps that much room.
 constexpr int kMaxPages = (INT_MAX - 8192) / kKv4Page;
+constexpr int kMaxEntries = INT_MAX - 2 * 65536;  // and room for two more per sequence
 
 // The cache and its tables as the kernels take them.
 int make_kv4(const vlm_kv4_cache* c, const int32_t* table, int max_pages, int n_seqs, const int32_t* lens, Kv4* out) {
@@ -52,7 +53,7 @@ int make_kv4(const vlm_kv4_cache* c, const int32_t* table, int max_pages, int n_
     return VLM_ERR_INVALID_ARG;
   VLM_TRY(check_heads(c->kv_heads, c->kv_heads, c->head_dim));
   if (c->n_pages <= 0 || c->n_pages > INT_MAX || n_seqs <= 0 || n_seqs > 65535 || max_pages <= 0 ||
-      max_pages > kMaxPages || static_cast<int64_t>(max_pages) * n_seqs > INT_MAX)
+      max_pages > kMaxPages || static_cast<int64_t>(max_pages) * n_seqs > kMaxEntries)
     return VLM_ERR_BAD_SHAPE;
   out->pages = static_cast<uint8_t*>(c->d_pages);
   out->n_pages = c->n_pages;
