@@ -58,6 +58,29 @@ def test_prompt_attention_scale_and_many_sequences():
     _run(lens, lens, 4, 2, 64, torch.bfloat16, scale=0.3)
 
 
+@pytest.mark.parametrize("lens,heads,kv_heads,dim", [
+    ([900] * 3 + [64] * 10, 32, 8, 64),          # 440 work items: the host chooses each one's CTA
+    ([900] * 3 + [64] * 19, 32, 8, 64),          # 512
+    ([900] * 3 + [64] * 20, 32, 8, 64),          # 520: dealt out in turn
+    ([2500] + [1] * 150, 8, 2, 128),             # few large ones among many small ones
+    ([1500, 3, 0, 701, 702], 16, 4, 128),
+    ([10] * 18 + [5000], 8, 8, 64),              # the largest share is one item's
+])
+def test_prompt_attention_does_not_depend_on_the_order_of_work(lens, heads, kv_heads, dim):
+    q = U.rand16(21, (sum(lens), heads, dim), torch.bfloat16).cuda()
+    k, v = (U.rand16(s, (sum(lens), kv_heads, dim), torch.bfloat16).cuda() for s in (22, 23))
+    out = torch.full_like(q, 7.0)
+    status = vlm.new_status()
+    vlm.prompt_attention(q, k, v, lens, out=out, status=status)
+    assert vlm.status_sync(status) == vlm.OK
+    at = 0
+    for n in lens:
+        rows = slice(at, at + n)
+        if n:
+            assert torch.equal(out[rows], vlm.prompt_attention(q[rows], k[rows], v[rows], [n]))
+        at += n
+
+
 def test_prompt_attention_of_column_blocks_into_a_strided_output():
     heads, kv_heads, dim, lens = 8, 2, 128, [77, 200]
     T_ = sum(lens)

@@ -9,7 +9,8 @@
 // (row = token * G + head), so both tiles, 2 TPT tokens, share every key and
 // value tile that is loaded, and a short prompt still fills its rows. CTAs
 // (one per SM, 512 TMEM columns) take items in turn, forwards and backwards
-// through the list, which is sorted by key tiles. 20 warps:
+// through the list, which is sorted by key tiles, or where there are few items
+// those that the host chose for them. 20 warps:
 //   warp 0       TMA: both Q tiles, then K and V tiles of 128 keys into two
 //                2-stage rings (128-byte swizzle, 64-column boxes).
 //   warps 1, 2   issue row tile t's products, one warp each, for key tile j
@@ -34,8 +35,8 @@
 // (N = 64 products) was slower. D = 64: the softmax itself, 2,500 cycles per key
 // tile. An item costs some 5,000 cycles besides: its last product, O to memory,
 // and the look at V below. Measured, 32/8 heads of 128, bf16: 4,096 tokens 112
-// to 116 us, 1,190 to 1,230 TFLOP/s (0.72 to 0.75 of the measured peak, by the box);
-// 8,192 tokens 411 to 425 us, 1,290 to 1,340;
+// to 118 us, 1,170 to 1,230 TFLOP/s (0.71 to 0.75 of the measured peak, by the box);
+// 8,192 tokens 411 to 425 us, 1,290 to 1,340; 3,241 tokens 80 to 83 us;
 // heads of 64: 8,192 tokens 367 to 373 us, 740. The softmax's instructions
 // count as well, 66% of the issue slots: exponentials from polynomials beside
 // the unit (2% slower), maxima exchanged on every tile instead of where one
@@ -54,6 +55,7 @@
 // and its key noted; at the end rows that do see a noted key add its values.
 // A query that sees no key (kv_len < q_len) gives 0.
 #include <algorithm>
+#include <functional>
 #include <numeric>
 #include <vector>
 
@@ -73,6 +75,8 @@ constexpr int kStages = 2;
 constexpr int kMaxSeqs = 256;    // sequences per launch (their table is a kernel argument)
 constexpr int kMaxOrder = 1024;  // tiles per key head whose order is passed along
 constexpr int kItemSlots = 512;  // items per CTA and launch
+constexpr int kMaxPacked = 512;  // items whose CTAs are chosen one by one
+constexpr int kMaxCtas = 256;     // and the CTAs then
 constexpr int kIssueRegs = 32, kSoftRegs = 112;
 static_assert(128 * kIssueRegs + 32 * kSoftWarps * kSoftRegs <= kThreads * 96, "the launch's registers");
 constexpr int kSets = 8;       // items whose noted keys are kept apart
@@ -84,6 +88,9 @@ struct SeqTable {
   int q0[kMaxSeqs], k0[kMaxSeqs], q_len[kMaxSeqs], kv_len[kMaxSeqs], tiles[kMaxSeqs];  // tiles: items per key head
   int ordered;               // pairs in `order`, or 0: sequence by sequence, last tile first
   uint32_t order[kMaxOrder];  // sequence << 16 | tile, the most key tiles first
+  // CTA b's items are item[first[b]] to item[first[b + 1] - 1], numbers in the launch's list;
+  // first[gridDim.x] is 0 where the list is dealt out in turn
+  uint16_t first[kMaxCtas + 1], item[kMaxPacked];
 };
 
 struct Args {
@@ -214,10 +221,20 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// The k-th item of this CTA in the launch's list, or n_items and more: CTAs take items in turn,
-// forwards and backwards, so that with items sorted by size every CTA's share is alike.
-__device__ __forceinline__ int nth_item(int k) {
+// How many of the launch's items are this CTA's, and the number of its k-th. Dealt out in
+// turn, forwards and backwards, so that with items sorted by size every CTA's share is
+// alike, or as the host chose.
+__device__ __forceinline__ bool chosen(const SeqTable& t) { return t.first[gridDim.x] != 0; }
+__device__ __forceinline__ int dealt(int k) {
   return k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+__device__ __forceinline__ int count_items(const SeqTable& t, int n_items) {
+  if (chosen(t)) return t.first[blockIdx.x + 1] - t.first[blockIdx.x];
+  const int rounds = n_items / static_cast<int>(gridDim.x);
+  return rounds + (dealt(rounds) < n_items ? 1 : 0);
+}
+__device__ __forceinline__ int nth_item(const SeqTable& t, int k) {
+  return chosen(t) ? t.item[t.first[blockIdx.x] + k] : dealt(k);
 }
 
 // A work item: sequence, key head, the first token of its row tiles, its key tiles.
@@ -304,11 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Decoding an item (divisions, indexed argument loads) takes some 2,000 cycles in
   // the middle of the pipeline, so it is done for the whole list at the start.
   Item* items_s = reinterpret_cast<Item*>(smem + C::kItems);
-  for (int k = threadIdx.x; k < kItemSlots; k += kThreads) {
-    const int idx = nth_item(k);
-    if (idx >= n_items) break;
-    items_s[k] = item_of(args, first_item + idx);
-  }
+  const int my_items = count_items(args.t, n_items);
+  for (int k = threadIdx.x; k < my_items; k += kThreads) items_s[k] = item_of(args, first_item + nth_item(args.t, k));
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
@@ -336,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_bytes = 128u * args.group * args.tpt * (D / 64);
       uint32_t kc = 0, vc = 0, qc = 0;
       bool ok = true;
-      for (int w = 0; ok && nth_item(w) < n_items; ++w) {
+      for (int w = 0; ok && w < my_items; ++w) {
         const Item it = items_s[w];
         const int n = it.n, tiles = it.tok(1, args.tpt) < it.q_len ? 2 : 1;
         if (n == 0) continue;
@@ -405,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_lag = t == 1 ? 0 : 1;
     uint32_t kc = 0, vc = 0, qc = 0;  // K, V and Q tiles so far (S and P run with K and V)
     bool ok = true;
-    for (int w = 0; ok && nth_item(w) < n_items; ++w) {
+    for (int w = 0; ok && w < my_items; ++w) {
       const Item it = items_s[w];
       const int n = it.n;
       if (n == 0) continue;
@@ -461,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // A warp whose wait failed keeps meeting its partner at the named barrier,
     // doing nothing else, so that the partner never waits for it.
-    for (; nth_item(items) < n_items; ++items) {
+    for (; items < my_items; ++items) {
       const Item it = items_s[items];
       const int tok = it.tok(t, args.tpt) + row_tok;
       const bool live = tok < it.q_len && row_tok < args.tpt;
@@ -677,6 +691,12 @@ bool smem_ready() {
   return true;
 }
 
+// Key tiles of tile `tile` of sequence i.
+int key_tiles(const SeqTable& t, int i, int tile, int tokens) {
+  const int end = t.kv_len[i] - t.q_len[i] + std::min(t.q_len[i], (tile + 1) * tokens);
+  return end <= 0 ? 0 : (end + BK - 1) / BK;
+}
+
 // Sorts all (sequence, tile) pairs by their key tiles, descending, where few
 // enough of them are passed along: dealt out forwards and backwards they then
 // load the CTAs alike. With more of them every CTA has so many items that the
@@ -687,10 +707,7 @@ int order_tiles(SeqTable& t, int tokens, int64_t pairs) {
   int most = 0;
   for (int i = 0; i < t.n; ++i) most = std::max(most, (t.kv_len[i] + BK - 1) / BK);
   if (most >= kLevels) return 0;
-  auto level = [&](int i, int tile) {
-    const int end = t.kv_len[i] - t.q_len[i] + std::min(t.q_len[i], (tile + 1) * tokens);
-    return end <= 0 ? 0 : (end + BK - 1) / BK;
-  };
+  auto level = [&](int i, int tile) { return key_tiles(t, i, tile, tokens); };
   int start[kLevels + 1];
   std::fill(start, start + most + 2, 0);
   for (int i = 0; i < t.n; ++i)
@@ -700,6 +717,81 @@ int order_tiles(SeqTable& t, int tokens, int64_t pairs) {
     for (int x = t.tiles[i] - 1; x >= 0; --x)
       t.order[start[most - level(i, x)]++] = static_cast<uint32_t>(i) << 16 | static_cast<uint32_t>(x);
   return static_cast<int>(pairs);
+}
+
+// Chooses the CTA of every item of a sorted list where each CTA gets only a few: dealt out
+// in turn, the third of three rounds lands on shares that are already equal (3,241 tokens,
+// 8 key heads: the largest share 12% above the mean). An item's cost is its key tiles and,
+// in quarters of one, item_cost. First every item goes, in order, to the CTA with the least
+// so far; where that leaves the largest share more than 4% above the least possible (at
+// 4,096 tokens, 2.7%, it measured 1% better than the other), every item goes to the
+// fullest CTA that has room for it under a limit, which is raised from the least possible
+// share until all fit. Dealt out and chosen: one image's prompt 86 and 80 us, nine ragged
+// prompts of heads of 64 54 and 45, 1,024 items of 8,192 tokens 423 and 426 (so not for
+// more than kMaxPacked). With 7 for heads of 128 86 and 436 us, with 10 for heads of 64 47.
+void choose_ctas(SeqTable& t, int tokens, int head_dim, int kv_heads, int ctas) {
+  const int item_cost = head_dim == 128 ? 10 : 7;
+  constexpr int kLevels = 2048;
+  const int items = t.ordered * kv_heads;
+  t.first[ctas] = 0;
+  if (t.ordered == 0 || items > kMaxPacked || items <= ctas || ctas > kMaxCtas) return;
+  int cost[kMaxPacked], sum = 0;
+  for (int p = 0; p < t.ordered; ++p)
+    for (int h = 0; h < kv_heads; ++h) {
+      cost[p * kv_heads + h] = 4 * key_tiles(t, t.order[p] >> 16, t.order[p] & 0xFFFF, tokens) + item_cost;
+      sum += cost[p * kv_heads + h];
+    }
+  const int least = std::max(cost[0], (sum + ctas - 1) / ctas);  // the largest share is at least this
+  uint8_t cta[kMaxPacked];
+  // the least loaded first: a heap of load << 8 | CTA
+  int heap[kMaxCtas];
+  for (int b = 0; b < ctas; ++b) heap[b] = b;
+  const auto more = std::greater<int>();
+  int most = 0;
+  for (int i = 0; i < items; ++i) {
+    std::pop_heap(heap, heap + ctas, more);
+    int& top = heap[ctas - 1];
+    cta[i] = static_cast<uint8_t>(top & 0xFF);
+    top += cost[i] << 8;
+    most = std::max(most, top >> 8);
+    std::push_heap(heap, heap + ctas, more);
+  }
+  if (most * 100LL > least * 104LL && most < kLevels) {
+    uint8_t fit[kMaxPacked];
+    int16_t bin[kLevels], next[kMaxCtas];  // CTAs by their room, in lists
+    for (int limit = least; limit < most; limit += 1 + limit / 128) {
+      uint64_t some[kLevels / 64] = {};  // which lists have one
+      std::fill(bin, bin + limit + 1, static_cast<int16_t>(-1));
+      auto put = [&](int b, int room) {
+        next[b] = bin[room];
+        bin[room] = static_cast<int16_t>(b);
+        some[room / 64] |= 1ull << (room % 64);
+      };
+      for (int b = ctas - 1; b >= 0; --b) put(b, limit);
+      int i = 0;
+      for (; i < items; ++i) {
+        int w = cost[i] / 64;
+        uint64_t bits = some[w] & (~0ull << (cost[i] % 64));
+        while (bits == 0 && ++w <= limit / 64) bits = some[w];
+        if (bits == 0) break;
+        const int room = 64 * w + __builtin_ctzll(bits), b = bin[room];
+        bin[room] = next[b];
+        if (bin[room] < 0) some[w] &= ~(1ull << (room % 64));
+        fit[i] = static_cast<uint8_t>(b);
+        put(b, room - cost[i]);
+      }
+      if (i < items) continue;
+      std::copy(fit, fit + items, cta);
+      break;
+    }
+  }
+  // by CTA, the largest first
+  int at[kMaxCtas + 1] = {};
+  for (int i = 0; i < items; ++i) ++at[cta[i] + 1];
+  if (*std::max_element(at, at + ctas + 1) > kItemSlots) return;
+  for (int b = 0; b < ctas; ++b) at[b + 1] += at[b];
+  for (int b = 0; b <= ctas; ++b) t.first[b] = static_cast<uint16_t>(at[b]);
+  for (int i = 0; i < items; ++i) t.item[at[cta[i]]++] = static_cast<uint16_t>(i);
 }
 
 // Tensor map of 16-bit [tokens, heads, D] with `stride` elements between
@@ -778,8 +870,10 @@ int launch_prompt_attention(const PromptAttn& p, cudaStream_t s) {
       a.out_stride = p.out_stride;
       a.status = p.status;
       for (int64_t at = 0; at < items;) {
-        const int n = static_cast<int>(std::min<int64_t>(items - at, static_cast<int64_t>(num_sms()) * kItemSlots));
-        const cudaError_t e = launch_pdl(kern, dim3(std::min(n, num_sms())), dim3(kThreads), smem, s, tq, tk, tv, a,
+        const int slots = std::min(num_sms(), kMaxCtas);
+        const int n = static_cast<int>(std::min<int64_t>(items - at, static_cast<int64_t>(slots) * kItemSlots));
+        choose_ctas(a.t, 2 * tpt, p.head_dim, p.kv_heads, std::min(n, slots));
+        const cudaError_t e = launch_pdl(kern, dim3(std::min(n, slots)), dim3(kThreads), smem, s, tq, tk, tv, a,
                                          static_cast<int>(at), n);
         if (e != cudaSuccess) return VLM_ERR_CUDA;
         at += n;
