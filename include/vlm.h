@@ -495,8 +495,8 @@ VLM_API int vlm_kv4_read(const vlm_kv4_cache* cache, const int32_t* d_table, int
  *   New token i sits at place len - q_len + i and sees the places up to its
  *   own; without any (len 0, or a place before 0) its row is 0.
  * d_q: [n_seqs * q_len] rows of heads * head_dim, strided by q_stride;
- * d_out: the same rows, contiguous, in dtype. q_len * (heads / kv_heads) at
- *   most 65535 (VLM_ERR_BAD_SHAPE).
+ * d_out: the same rows, contiguous, in dtype; must not overlap any other buffer
+ *   of the call. q_len * (heads / kv_heads) at most 65535 (VLM_ERR_BAD_SHAPE).
  * d_weights: NULL, or device fp32 [n_seqs][kv_heads][max_pages * 64]:
  *   weights[s][h][j] += the softmax weights of place j summed over the q_len
  *   tokens and the query heads of key head h, for j < len; without atomics,
