@@ -868,10 +868,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, kCt
   pr.drain();
 }
 
-// Joins the partial sums of one row of a unit that was cut: a CTA per row, of two
-// warps where a unit has a dozen parts at most, else of eight. All
-// the runs' factors first, one run per thread, then their O rows strided over
-// the warps, each lane four columns, eight loads under way at a time.
+// Joins the partial sums of one row of a unit that was cut: a CTA of two or eight
+// warps per row. All the runs' factors first, one run per thread, then their O
+// rows strided over the warps, each lane four columns, eight loads under way at
+// a time.
 template <typename T, int D, int kJoinWarps>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv4_combine_kernel(const Args a) {
   griddep_wait();
@@ -1145,7 +1145,12 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
   auto pick = [&](auto type, auto dim, auto nt) {
     using T = decltype(type);
     constexpr int D = decltype(dim)::value, NT = decltype(nt)::value;
-    const bool few = a.runs <= 12LL * z.seqs * c0.kv_heads * a.row_tiles;
+    // two warps per joined row where a unit has a dozen parts at most, or where the rows fill
+    // the SMs anyway: with eight 24 sequences of 3,000 places, 16 rows of 64, 23.9 and not
+    // 20.6 us, 16 of 9,000, 16 rows of 128, 61.5 and not 55.5; with two always 24 of 3,000,
+    // 4 rows of 64, 20.6 and not 18.6
+    const int64_t rows_in_all = static_cast<int64_t>(z.seqs) * c0.kv_heads * a.rows;
+    const bool few = a.runs <= 12LL * z.seqs * c0.kv_heads * a.row_tiles || rows_in_all > 8LL * num_sms();
     return run(kv4_attn_kernel<T, D, NT>, kv4_cluster_attn_kernel<T, D, NT>, few ? kv4_combine_kernel<T, D, 2> : kv4_combine_kernel<T, D, 8>, few ? 64 : 256,
                kv4_weights_kernel<T, D, NT>, 2, smem_ready<T, D, NT>());
   };
