@@ -110,8 +110,9 @@ struct Cfg {
   static constexpr int kTile = kSub * (D / 64);    // one Q, K or V tile
   static constexpr int kQ = 0, kK = 2 * kTile, kV = kK + kStages * kTile;
   static constexpr int kBars = kV + kStages * kTile;
-  static constexpr int kXch = kBars + 256;         // row maxima [tile][parity][half][row], sums [tile][half][row]
-  static constexpr int kFlags = kXch + (8 + 4) * kRows * 4;  // noted keys, kSets sets of 512 bits
+  // row maxima [tile][parity of the key tile][half][row], sums [tile][parity of the item][half][row]
+  static constexpr int kXch = kBars + 256;
+  static constexpr int kFlags = kXch + (8 + 8) * kRows * 4;  // noted keys, kSets sets of 512 bits
   static constexpr int kItems = kFlags + kSets * 64;         // this CTA's first items, decoded
   static constexpr int kSmem = kItems + kItemSlots * 32 + 1024;
   static constexpr uint32_t s_col(int t) { return D == 128 ? 0 : 128 * t; }
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = (warp - 4 - 8 * t) * 32 + lane;  // 0..255 in the row tile's threads
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     float* xmax = reinterpret_cast<float*>(smem + C::kXch) + t * 4 * kRows;
-    float* xsum = reinterpret_cast<float*>(smem + C::kXch) + 8 * kRows + t * 2 * kRows;
+    float* xsum0 = reinterpret_cast<float*>(smem + C::kXch) + (8 + t * 4) * kRows;
     const uint64_t sl2x2 = pair_f32(args.sl2);
     const float grow_by = fminf(kRescaleThreshold / args.sl2, 1e38f);  // in the logits' own units, as the maximum is
     const int row_tok = r / args.group, row_head = r - row_tok * args.group;
@@ -611,6 +612,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(smem_u32(p_full + t), lane);
         ++oc;
       }
+      // By the item's parity: a warp that is done with an item without key tiles, or with one key tile and
+      // an idle row tile (neither meets its partner before this), must not write over the sum that the
+      // partner still has to read from the item before. Two items on, the barrier of the one between is passed.
+      float* xsum = xsum0 + (items & 1) * 2 * kRows;
       xsum[hf * kRows + r] = l;
       bar_sync(pair_id, 64);
       l += xsum[(hf ^ 1) * kRows + r];
