@@ -30,3 +30,27 @@ def test_short_items_behind_long_ones_keep_their_rows_sums(q_lens, kv_lens, head
         rows, keys = slice(q0, q0 + m), slice(k0, k0 + n)
         assert torch.equal(runs[0][rows], vlm.prompt_attention(q[rows], k[keys], v[keys], [m], [n]))
         q0, k0 = q0 + m, k0 + n
+
+
+@pytest.mark.parametrize("q_len,kv_len,heads,kv_heads", [
+    (256, 256, 2, 2),    # 128 tokens per row tile: the first keys' tile is the first row tile's last, and whole to the second
+    (128, 168, 8, 2),    # 32 tokens per row tile
+    (168, 199, 6, 2),    # 42
+])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_a_value_replaced_for_one_row_tile_is_replaced_for_both(q_len, kv_len, heads, kv_heads, dim, dtype):
+    # The weights of key 5 round to 0: where its infinite value is replaced and noted the rows get infinity, where the
+    # product reads it NaN. Both row tiles of an item have to do the same, whichever comes first.
+    q = U.rand16(81, (q_len, heads, dim), dtype)
+    k, v = (U.rand16(s, (kv_len, kv_heads, dim), dtype) for s in (82, 83))
+    q[..., 0], k[..., 0], k[5, :, 0], v[5, :, 7] = 8.0, 0.0, -1000.0, float("inf")
+    args = [x.cuda() for x in (q, k, v)]
+    runs = [vlm.prompt_attention(*args, [q_len], [kv_len]) for _ in range(20)]
+    for r in runs[1:]:
+        assert torch.equal(r.view(torch.int16), runs[0].view(torch.int16))
+    sees = max(0, 5 - (kv_len - q_len))  # the first query that sees key 5
+    got = runs[0].float().cpu()
+    assert torch.isfinite(got[:sees]).all()
+    assert (got[sees:, :, 7] == float("inf")).all()
+    assert torch.isfinite(got[:, :, [c for c in range(dim) if c != 7]]).all()

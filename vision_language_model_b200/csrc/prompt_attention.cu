@@ -49,10 +49,12 @@
 // Roundings: P to the inputs' type (half a step; P <= 2^8 and its fp32 sum is
 // taken before rounding), the output once; everything else is fp32.
 // Places that a row does not see get weight 0. A weight of 0 does not stop an
-// infinity or NaN in V, so on key tiles that some row does not see in full the
-// softmax threads look V over in shared memory before the product: rows behind
-// the sequence's keys become 0, and a value that is not finite is replaced by 0
-// and its key noted; at the end rows that do see a noted key add its values.
+// infinity or NaN in V, so on key tiles that some row of the item does not see in
+// full the softmax threads of both row tiles look V over in shared memory before
+// their product: rows behind the sequence's keys become 0, and a value that is not
+// finite is replaced by 0 and its key noted; at the end rows that do see a noted
+// key add its values. (On other key tiles the product takes it, with NaN where the
+// row's weight rounds to 0.)
 // A query that sees no key (kv_len < q_len) gives 0.
 #include <algorithm>
 #include <functional>
@@ -482,7 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = tok < it.q_len && row_tok < args.tpt;
       const int lim = it.shift + tok + 1;                     // the row sees keys [0, lim)
       const int lim_min = it.shift + it.tok(t, args.tpt) + 1;  // what every row of the tile sees
-      const int flag_base = max(0, it.shift + it.tok0 + 1) / BK * BK;
+      const int lim_item = it.shift + it.tok0 + 1;             // and every row of the item
+      const int flag_base = max(0, lim_item) / BK * BK;
       // The row tiles' threads are at most three key tiles apart (two K stages and the
       // alternation of S), so the notes of four items back are no longer in use: cleared
       // here for the item four ahead. Items without keys have no notes and do not count.
@@ -563,9 +566,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st32(col, o);
           }
         }
-        if (masked) {
-          // Look this V tile over before its product. Both row tiles' threads do so; what
-          // one writes the other would write as well.
+        if ((j + 1) * BK > lim_item) {
+          // Look this V tile over before its product. Both row tiles' threads do so, the second's
+          // also where its own rows see the whole tile: its product would otherwise read values
+          // that the first one's threads are replacing. What one writes the other would write as well.
           const uint32_t vc = vc_item + j, vs = vc % kStages;
           ok = mbar_wait_warp(smem_u32(v_full + vs), (vc / kStages) & 1, abort_v, args.status);
           if (ok) {
@@ -604,6 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
+            // also for what the other row tile's threads wrote and this one found done
             fence_proxy_async_smem();
           }
         }
