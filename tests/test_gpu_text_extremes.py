@@ -1,0 +1,55 @@
+"""The text side's attention where numbers get extreme: large logits, many small weights, infinities."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import text_oracle as T
+from tests import text_util as U
+from tests.gpu_util import guarded_copy
+from vision_language_model_b200 import vlm
+
+pytestmark = pytest.mark.gpu
+PAGE, K_SG, V_SG = U.PAGE, U.K_SG, U.V_SG
+
+
+def _steep(seed, lens, kv_heads, dim, width):
+    """A pool whose keys differ in column 1 alone as far as the queries of _steep_q go: their products are
+    24 and a little, sums of two terms with 20 bits between them, so fp32 holds every one exactly."""
+    pages, table, _ = U.random_pool(seed, lens, kv_heads, dim, width=width)
+    (at, n, w), scales = T._parts(dim)[0], T._parts(dim)[2]
+    rows = pages[..., at:at + n].reshape(*pages.shape[:2], PAGE, w)
+    rows[..., 0] = (rows[..., 0] & 0xF0) | 7  # column 0: 6
+    pages[..., at:at + n] = rows.reshape(*pages.shape[:2], n)
+    pages[..., scales[0]:scales[0] + scales[1]:scales[2]] = 0x48  # times 4
+    return pages, table
+
+
+@pytest.mark.parametrize("size", [4096.0, 2.0 ** 20, 2.0 ** 26])
+@pytest.mark.parametrize("lens,heads,kv_heads,dim,q_len,dtype", [
+    ([700, 65], 4, 2, 128, 1, torch.bfloat16),
+    ([700, 65], 16, 2, 64, 2, torch.float16),
+    ([400], 40, 1, 64, 1, torch.bfloat16),     # several row tiles: the weights in a launch of their own
+    ([1300, 0, 3], 8, 4, 128, 3, torch.float16),
+])
+@pytest.mark.parametrize("width", [128, 140])  # by clusters, and by runs that a join puts together
+def test_weights_and_outputs_of_large_logits(lens, heads, kv_heads, dim, q_len, dtype, size, width):
+    # logits of `size` in log2 units that differ by 4096 -> 0.005, 2^20 -> 1.3, 2^26 -> 85 per step of a code
+    pages, table = _steep(41, lens, kv_heads, dim, width)
+    q = torch.zeros((len(lens) * q_len, heads, dim), dtype=dtype)
+    q[..., 0], q[..., 1] = 4.0, 4.0 * 2.0 ** -16
+    scale = float(np.float32(size * np.log(2.0) / (4.0 * 24.0 * K_SG)))
+    o, a, w = T.cache_attention(pages, table, lens, q.float().numpy(), q_len, K_SG, V_SG, scale)
+    status = vlm.new_status()
+    gw = guarded_copy(torch.zeros((len(lens), kv_heads, width * PAGE)))
+    got = vlm.kv4_attention(guarded_copy(torch.from_numpy(pages)), U.cuda_int(table), U.cuda_int(lens), guarded_copy(q),
+                            K_SG, V_SG, scale=scale, weights=gw, status=status)
+    assert vlm.status_sync(status) == vlm.OK
+    # A difference of two products is exact; its factor takes four roundings (and the product one), so a weight of
+    # 2^-60 or more is off by 60 * 5 * 2^-24 ln 2, by 2^-21 of the exponential, and as much again where a run's
+    # sums are joined; its sum by 2^-24 per term.
+    e = 2 * (60 * 5 * 2.0 ** -24 * np.log(2.0) + 2.0 ** -21) + (max(lens) + 8) * 2.0 ** -24
+    rows = heads // kv_heads * q_len
+    U.assert_close(gw, w, (2 * e + rows * 2.0 ** -24) * w + rows * 2.0 ** -60, "weights")
+    u = U.half_step(dtype)
+    U.assert_close(got, o, u * np.abs(o) + (2.0 ** -11 + 2 * e) * a * (1 + u) + 2.0 ** -32 * max(lens) * 720 * V_SG +
+                   float(torch.finfo(dtype).smallest_normal) * u, "output")

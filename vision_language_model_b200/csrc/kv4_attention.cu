@@ -92,8 +92,8 @@ struct Args {
   void* out;         // [n_seqs * q_len, heads, D]
   int32_t* prefix;   // [n_seqs + 1] sequences' offsets in the cut, written by the first kernel's CTA 0
   float* part_o;     // [2 * runs][tile_rows][D]
-  float2* part_ml;   // [2 * runs][tile_rows] maximum (log2 units) and sum
-  float* lse;        // [n_seqs, kv_heads, rows] log2 of a row's sum (null: not wanted)
+  float4* part_ml;   // [2 * runs][tile_rows] maximum of the products (-inf: none seen), sum, the row's factor
+  float2* stats;     // [n_seqs, kv_heads, rows] a row's maximum and 1 / its sum (null: not wanted)
   float* weights;    // [n_seqs, kv_heads, max_pages * 64]
   int runs;          // warps of the first kernel
   int32_t* status;
@@ -463,6 +463,14 @@ __device__ __forceinline__ void init_smem(Smem<D>& sm, int warp, int lane) {
   if (threadIdx.x == 0) sm.abort_flag = 0;
 }
 
+// What a weight is made of again: 2^((product - maximum) factor) / sum. Maxima are
+// joined and kept as products: a rounded maximum in log2 units would be off by
+// 2^-24 of itself, and the log of the sum lost beside it, which counts from logits
+// of some 10^3 on and makes equal places of large ones weigh 1 each.
+__device__ __forceinline__ float2 row_stats(float top, float sum) {
+  return make_float2(top, sum == 0.0f ? 0.0f : 1.0f / sum);
+}
+
 template <int D, int NT>
 __device__ __forceinline__ void clear(State<D, NT>& z) {
 #pragma unroll
@@ -587,7 +595,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Ar
         for (int o = 4; o < 32; o <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
         const int tr = 8 * n + 2 * c + r, row = at.tile * kTileRows + tr;
         if (row >= a.rows) continue;
-        const float m = z.m[n][r] == kNoMax ? -INFINITY : z.m[n][r] * factor[n][r];  // log2 units
         // columns g D / 8 + 2 j (elements r) and + 1 (elements 2 + r) of tile j
         if (whole) {
           const float inv = l[r] == 0.0f ? 0.0f : a.c.v_sg / l[r];
@@ -601,16 +608,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Ar
                            pack16<T>(z.o[n][j + 1][r] * inv, z.o[n][j + 1][2 + r] * inv),
                            pack16<T>(z.o[n][j + 2][r] * inv, z.o[n][j + 2][2 + r] * inv),
                            pack16<T>(z.o[n][j + 3][r] * inv, z.o[n][j + 3][2 + r] * inv));
-          if (g == 0 && a.lse != nullptr)
-            a.lse[(static_cast<int64_t>(at.s) * a.c.kv_heads + at.kvh) * a.rows + row] =
-                l[r] == 0.0f ? INFINITY : m + log2f(l[r]);
+          if (g == 0 && a.stats != nullptr)
+            a.stats[(static_cast<int64_t>(at.s) * a.c.kv_heads + at.kvh) * a.rows + row] = row_stats(z.m[n][r], l[r]);
         } else {
           float* dst = a.part_o + (slot * kTileRows + tr) * D + g * (D / 8);
 #pragma unroll
           for (int j = 0; j < D / 16; j += 2)
             *reinterpret_cast<float4*>(dst + 2 * j) =
                 make_float4(z.o[n][j][r], z.o[n][j][2 + r], z.o[n][j + 1][r], z.o[n][j + 1][2 + r]);
-          if (g == 0) a.part_ml[slot * kTileRows + tr] = make_float2(m, l[r]);
+          if (g == 0)
+            a.part_ml[slot * kTileRows + tr] =
+                make_float4(z.m[n][r] == kNoMax ? -INFINITY : z.m[n][r], l[r], factor[n][r], 0.0f);
         }
       }
     }
@@ -630,13 +638,13 @@ __device__ __forceinline__ void weights_before(const float* dst, int first, int 
   for (int h = 0; h < 2; ++h) before[h] = own_place<D>(first, h) < len ? dst[own_place<D>(first, h)] : 0.0f;
 }
 
-// dst[j] = before + the sum over the rows of 2^(logit - norm) for the places of a page:
-// the logits once more from its keys. rows_of(tile) sets the rows of a row tile, where
-// there are several.
+// dst[j] = before + the sum over the rows of 2^((product - top) factor) inv for the places
+// of a page: the products once more from its keys. rows_of(tile) sets the rows of a row
+// tile, where there are several.
 template <int D, int NT, typename Rows>
 __device__ __forceinline__ void weigh_page(const uint8_t* page, int first, int len, int row_tiles, Rows rows_of,
                                            const uint32_t (&qf)[NT][D / 16][2], const float (&factor)[NT][2],
-                                           const float (&norm)[NT][2], const int (&seen)[NT][2],
+                                           const float2 (&stats)[NT][2], const int (&seen)[NT][2],
                                            const float (&before)[2], float* dst) {
   using M = Map<D>;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -655,8 +663,8 @@ __device__ __forceinline__ void weigh_page(const uint8_t* page, int first, int l
           const int j = first + 32 * h + 16 * y + M::token(e >> 1, g >> 1, g & 1);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const float p2 = ex2(__fmul_rn(s[y][n][e], factor[n][e & 1]) - norm[n][e & 1]);
-            w[y][e >> 1] += j < seen[n][e & 1] ? p2 : 0.0f;
+            const float p2 = ex2((s[y][n][e] - stats[n][e & 1].x) * factor[n][e & 1]);
+            w[y][e >> 1] += j < seen[n][e & 1] ? p2 * stats[n][e & 1].y : 0.0f;
           }
         }
     }
@@ -780,7 +788,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, kCt
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
       const int tr = 8 * n + 2 * c + r;
-      if (g == 0) ml[warp][tr] = make_float2(z.m[n][r] == kNoMax ? -INFINITY : z.m[n][r] * factor[n][r], l[r]);
+      if (g == 0) ml[warp][tr] = make_float2(z.m[n][r] == kNoMax ? -INFINITY : z.m[n][r], l[r]);
 #pragma unroll
       for (int j = 0; j < D / 16; j += 2)
         *reinterpret_cast<float4*>(own + tr * D + g * (D / 8) + 2 * j) =
@@ -801,7 +809,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, kCt
     float top = part.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float f = part.x == top ? 1.0f : ex2(part.x - top);
+    // the factor of row tr, which the lanes of column group rank / 2 have
+    const float scale = __shfl_sync(0xffffffffu, (rank & 1) ? factor[n][1] : factor[n][0], rank >> 1);
+    const float f = part.x == top ? 1.0f : ex2((part.x - top) * scale);
     float sum = part.y * f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -834,21 +844,22 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, kCt
                       lane * 4,
                   t.x * inv, t.y * inv, t.z * inv, t.w * inv);
       }
-      if (a.lse != nullptr && lane == 0)
-        a.lse[(static_cast<int64_t>(s) * a.c.kv_heads + kvh) * a.rows + row] = sum == 0.0f ? INFINITY : top + log2f(sum);
+      if (a.stats != nullptr && lane == 0)
+        a.stats[(static_cast<int64_t>(s) * a.c.kv_heads + kvh) * a.rows + row] = row_stats(top, sum);
     }
     __syncthreads();
   }
-  cluster_sync_all();  // the others have read this CTA's sums, and every row's lse is written
+  cluster_sync_all();  // the others have read this CTA's sums, and every row's stats are written
   if (!weigh) return;
   fence_proxy_async_smem();
-  float norm[NT][2];
+  float2 stats[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = 8 * n + 2 * c + r;
-      norm[n][r] = row < a.rows ? a.lse[(static_cast<int64_t>(s) * a.c.kv_heads + kvh) * a.rows + row] : INFINITY;
+      stats[n][r] = row < a.rows ? a.stats[(static_cast<int64_t>(s) * a.c.kv_heads + kvh) * a.rows + row]
+                                 : make_float2(0.0f, 0.0f);
       if (row >= a.rows) seen[n][r] = 0;
     }
   float* dst = a.weights + (static_cast<int64_t>(s) * a.c.kv_heads + kvh) * a.c.max_pages * kKv4Page;
@@ -861,7 +872,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, kCt
     float before[2];
     weights_before<D>(dst, first, len, before);
     if (!pr.wait(abort_v, a.status)) break;
-    weigh_page<D, NT>(ring + pr.taken % M::kStages * L::kBytes, first, len, 1, [](int) {}, qf, factor, norm, seen, before, dst);
+    weigh_page<D, NT>(ring + pr.taken % M::kStages * L::kBytes, first, len, 1, [](int) {}, qf, factor, stats, seen, before, dst);
     ++pr.taken;
     __syncwarp();
   }
@@ -889,9 +900,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_combine_kernel(const Args
   const int span = a.prefix[s + 1] - a.prefix[s];
   const int64_t lo = static_cast<int64_t>(a.prefix[s]) * per_seq + static_cast<int64_t>(kvh * a.row_tiles + tile) * span;
   const int i0 = static_cast<int>((lo + kUnitPages) / chunk), i1 = static_cast<int>((lo + span - 1) / chunk);
-  float* lse = a.lse == nullptr ? nullptr : a.lse + (static_cast<int64_t>(s) * a.c.kv_heads + kvh) * a.rows + row;
+  float2* stats = a.stats == nullptr ? nullptr : a.stats + (static_cast<int64_t>(s) * a.c.kv_heads + kvh) * a.rows + row;
   if (span == 0) {
-    if (lse != nullptr && threadIdx.x == 0) *lse = INFINITY;
+    if (stats != nullptr && threadIdx.x == 0) *stats = make_float2(0.0f, 0.0f);
     return;
   }
   if (i0 == i1) return;  // one run held the unit: done there
@@ -899,13 +910,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_combine_kernel(const Args
   auto at = [&](int i) {
     return (2 * static_cast<int64_t>(i) + (i * chunk >= lo ? 0 : 1)) * a.tile_rows + r;
   };
+  const float scale = a.part_ml[at(i0)].z;  // the row's, in every part
   float top = -INFINITY, sum = 0.0f;
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
   const bool mine = lane * 4 < D;
   for (int base = i0; base <= i1; base += kJoinThreads) {  // as a rule once
     const int n = min(kJoinThreads, i1 - base + 1);
     float2 ml = make_float2(-INFINITY, 0.0f);
-    if (static_cast<int>(threadIdx.x) < n) ml = a.part_ml[at(base + threadIdx.x)];
+    if (static_cast<int>(threadIdx.x) < n) ml = *reinterpret_cast<const float2*>(a.part_ml + at(base + threadIdx.x));
     float m = ml.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -915,8 +927,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_combine_kernel(const Args
     m = top;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, sm_red[w]);
-    const float rescale = top == m ? 1.0f : ex2(top - m);
-    const float f = ml.x == m ? 1.0f : ex2(ml.x - m);
+    const float rescale = top == m ? 1.0f : ex2((top - m) * scale);
+    const float f = ml.x == m ? 1.0f : ex2((ml.x - m) * scale);
     factor[threadIdx.x] = f;
     top = m;
     sum = sum * rescale + ml.y * f;
@@ -954,10 +966,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_combine_kernel(const Args
                   ((static_cast<int64_t>(s) * a.q_len + row / a.group) * a.heads + kvh * a.group + row % a.group) * D +
                   lane * 4,
               t.x * inv, t.y * inv, t.z * inv, t.w * inv);
-  if (lse != nullptr && lane == 0) *lse = sum == 0.0f ? INFINITY : top + log2f(sum);
+  if (stats != nullptr && lane == 0) *stats = row_stats(top, sum);
 }
 
-// weights[s, kvh, j] += sum over the rows of 2^(logit - lse): the logits once
+// weights[s, kvh, j] += sum over the rows of 2^(logit - maximum) / sum: the logits once
 // more from the keys alone (half the cache's bytes; storing them in the first
 // kernel would cost 8 bytes per row and token). One warp owns a slice and sums
 // its rows in a fixed order, so no atomics.
@@ -996,10 +1008,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_weights_kernel(const
     int next = 0;
     for (; next < min(mine, M::kStages); ++next) issue(next);
     const int open = len - a.q_len + 1;
-    const float* lse = a.lse + (static_cast<int64_t>(at.s) * a.c.kv_heads + at.kvh) * a.rows;
+    const float2* of_row = a.stats + (static_cast<int64_t>(at.s) * a.c.kv_heads + at.kvh) * a.rows;
     float* dst = a.weights + (static_cast<int64_t>(at.s) * a.c.kv_heads + at.kvh) * a.c.max_pages * kKv4Page;
     uint32_t qf[NT][M::kSteps][2];
-    float factor[NT][2], norm[NT][2];
+    float factor[NT][2];
+    float2 stats[NT][2];
     int seen[NT][2];
     auto rows_of = [&](int tile) {
       load_q<T, D, NT>(a, at.s, at.kvh, tile * 8 * NT, qf, factor);
@@ -1008,7 +1021,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_weights_kernel(const
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int row = tile * 8 * NT + 8 * n + 2 * c + r;
-          norm[n][r] = row < a.rows ? lse[row] : INFINITY;
+          stats[n][r] = row < a.rows ? of_row[row] : make_float2(0.0f, 0.0f);
           seen[n][r] = row < a.rows ? open + row / a.group : 0;
         }
     };
@@ -1020,7 +1033,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_weights_kernel(const
       weights_before<D>(dst, first, len, before);
       ok = pr.wait(abort_v, a.status);
       if (!ok) break;
-      weigh_page<D, NT>(ring + pr.taken % M::kStages * L::kBytes, first, len, a.row_tiles, rows_of, qf, factor, norm,
+      weigh_page<D, NT>(ring + pr.taken % M::kStages * L::kBytes, first, len, a.row_tiles, rows_of, qf, factor, stats,
                         seen, before, dst);
       ++pr.taken;
       __syncwarp();
@@ -1062,8 +1075,8 @@ namespace {
 // operand made from codes); the CTAs; the workspace's parts.
 struct Shape {
   int tile_rows, grid, seqs;
-  size_t prefix, part_o, part_ml, lse;
-  size_t total() const { return prefix + part_o + part_ml + lse; }
+  size_t prefix, part_o, part_ml, stats;
+  size_t total() const { return prefix + part_o + part_ml + stats; }
 };
 Shape shape_of(int n_seqs, int heads, int rows, int head_dim, int q_len) {
   Shape z;
@@ -1073,8 +1086,8 @@ Shape shape_of(int n_seqs, int heads, int rows, int head_dim, int q_len) {
   const size_t slots = 2 * static_cast<size_t>(z.grid) * kWarps * z.tile_rows;
   z.prefix = up((static_cast<size_t>(z.seqs) + 1) * 4);
   z.part_o = up(slots * head_dim * 4);
-  z.part_ml = up(slots * 8);
-  z.lse = up(static_cast<size_t>(z.seqs) * heads * q_len * 4);
+  z.part_ml = up(slots * 16);
+  z.stats = up(static_cast<size_t>(z.seqs) * heads * q_len * 8);
   return z;
 }
 }  // namespace
@@ -1102,8 +1115,8 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.prefix = reinterpret_cast<int32_t*>(w);
   a.part_o = reinterpret_cast<float*>(w + z.prefix);
-  a.part_ml = reinterpret_cast<float2*>(w + z.prefix + z.part_o);
-  a.lse = weights == nullptr ? nullptr : reinterpret_cast<float*>(w + z.prefix + z.part_o + z.part_ml);
+  a.part_ml = reinterpret_cast<float4*>(w + z.prefix + z.part_o);
+  a.stats = weights == nullptr ? nullptr : reinterpret_cast<float2*>(w + z.prefix + z.part_o + z.part_ml);
   const size_t smem = kWarps * (head_dim == 128 ? Map<128>::kRing : Map<64>::kRing) +
                       (static_cast<size_t>(z.seqs) + 1) * 4;
   // A small batch goes by clusters, no warp with more than a few pages: where all units'
