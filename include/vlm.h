@@ -495,7 +495,10 @@ VLM_API int vlm_kv4_read(const vlm_kv4_cache* cache, const int32_t* d_table, int
  *
  * d_lens: device int32 [n_seqs], tokens in the cache, the new ones included.
  *   New token i sits at place len - q_len + i and sees the places up to its
- *   own; without any (len 0, or a place before 0) its row is 0.
+ *   own; without any (len 0, or a place before 0) its row is 0. Sums are fp32;
+ *   a weight is rounded to 11 bits (below 2^-21 of its row's largest to within
+ *   2^-32 of that), a query's values below 2^-14 of its largest to within 2^-25
+ *   of that.
  * d_q: [n_seqs * q_len] rows of heads * head_dim, strided by q_stride;
  * d_out: the same rows, contiguous, in dtype; must not overlap any other buffer
  *   of the call. q_len * (heads / kv_heads) at most 65535 (VLM_ERR_BAD_SHAPE).

@@ -53,3 +53,33 @@ def test_weights_and_outputs_of_large_logits(lens, heads, kv_heads, dim, q_len, 
     u = U.half_step(dtype)
     U.assert_close(got, o, u * np.abs(o) + (2.0 ** -11 + 2 * e) * a * (1 + u) + 2.0 ** -32 * max(lens) * 720 * V_SG +
                    float(torch.finfo(dtype).smallest_normal) * u, "output")
+
+
+@pytest.mark.parametrize("gap", [20.6, 25.5])
+@pytest.mark.parametrize("dim,dtype", [(64, torch.bfloat16), (128, torch.float16)])
+def test_many_small_weights_beside_a_large_one(dim, dtype, gap):
+    # 131,072 places, the first with 2^gap times the others' weight and a value of 0, so the others are the whole
+    # output. So many sequences (sharing two pages) that most are one warp's: it keeps the first place's maximum.
+    S, kv_heads, n = 250, 8, 131072
+    pages = np.random.default_rng(7).integers(0, 256, (2, kv_heads, T.page_bytes(dim)), dtype=np.uint8)
+    pages[..., PAGE * dim:] = 0x48
+    (ka, kn, kw), (va, vn, vw) = T._parts(dim)[:2]
+    pages[..., ka:ka + kn] = 0
+    pages[..., va:va + vn] &= 0x77  # values >= 0: nothing cancels
+    pages[0, :, ka], pages[0, :, va:va + vw] = 7, 0
+    table = np.ones((S, n // PAGE), np.int32)
+    table[:, 0] = 0
+    q = torch.zeros((S, kv_heads, dim), dtype=dtype)
+    q[..., 0] = 1.0
+    scale = float(np.float32(gap * np.log(2.0) / (24.0 * K_SG)))
+    o, a, _ = T.cache_attention(pages, table[:1], [n], q[:1].float().numpy(), 1, K_SG, V_SG, scale)
+    status = vlm.new_status()
+    got = vlm.kv4_attention(guarded_copy(torch.from_numpy(pages)), U.cuda_int(table), U.cuda_int([n] * S), q.cuda(), K_SG,
+                            V_SG, scale=scale, status=status)
+    assert vlm.status_sync(status) == vlm.OK
+    # P rounded to fp16 (half a step; weights under 2^-21 of the largest by 2^-32 of it), exponentials of exact
+    # logits (the factor's and the product's roundings, the unit's 2^-21), fp32 sums of a lane's share of the places
+    u = U.half_step(dtype)
+    e = 2.0 ** -11 + 2 * (gap * 5 * 2.0 ** -24 + 2.0 ** -21) + 2 * (n // 4) * 2.0 ** -24
+    tol = u * np.abs(o) + e * a * (1 + u) + 2.0 ** -32 * n * 24 * V_SG + float(torch.finfo(dtype).smallest_normal) * u
+    U.assert_close(got, np.broadcast_to(o, got.shape), np.broadcast_to(tol, got.shape))

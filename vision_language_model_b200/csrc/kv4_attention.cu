@@ -24,8 +24,12 @@
 //     2^-14 of the row's largest lose bits, 2^-25 of the largest at most --
 //     what an fp32 sum loses as well. The global scales, 1 / that power and
 //     log2(e) are one fp32 factor of the logit.
-//   - P is rounded to fp16 for the second product (half a step, 2^-11); the
-//     sum of a row's weights, its maximum and both products' sums stay in fp32.
+//   - P is rounded to fp16 for the second product. It is made 2^7 times as large,
+//     up to fp16's largest powers of two: half a step, 2^-11, down to 2^-21 of the
+//     row's largest weight so far, and 2^-32 of that below, so that a long tail of
+//     small weights beside a large one keeps its sum (made as it is, everything
+//     under 2^-25 became 0). The sum of a row's weights, its maximum and both
+//     products' sums stay in fp32.
 //   - Work is cut into equal runs of pages, one per warp, over the flattened
 //     (sequence, key head, row tile, page) list, whatever the lengths (a unit's
 //     start counts as two pages more), computed on the device from the lengths
@@ -63,7 +67,8 @@ constexpr int kMinPages = 1;  // of a run: a page takes a warp about 1 us, joini
 constexpr int kUnitPages = 2;  // pages that starting a unit counts as where the work is cut
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNoMax = -3.0e38f;  // a row's maximum before it sees a place; finite, so that -inf minus it is no NaN
-constexpr float kRescale = 8.0f;  // log2 units; P stays below 2^8
+constexpr float kRescale = 8.0f;  // log2 units; weights stay below 2^8 of their maximum
+constexpr float kLift = 7.0f;     // log2 units that P, O and the sums are larger by: P stays below 2^15
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -93,7 +98,7 @@ struct Args {
   int32_t* prefix;   // [n_seqs + 1] sequences' offsets in the cut, written by the first kernel's CTA 0
   float* part_o;     // [2 * runs][tile_rows][D]
   float4* part_ml;   // [2 * runs][tile_rows] maximum of the products (-inf: none seen), sum, the row's factor
-  float2* stats;     // [n_seqs, kv_heads, rows] a row's maximum and 1 / its sum (null: not wanted)
+  float2* stats;     // [n_seqs, kv_heads, rows] a row's maximum and 1 / its sum of weights (null: not wanted)
   float* weights;    // [n_seqs, kv_heads, max_pages * 64]
   int runs;          // warps of the first kernel
   int32_t* status;
@@ -390,13 +395,14 @@ __device__ __forceinline__ void take(const uint8_t* page, int x0, int first, int
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const uint64_t f2 = pack2(__float_as_uint(factor[n][0]), __float_as_uint(factor[n][1]));
-    const uint64_t negm = pack2(__float_as_uint(-z.m[n][0]), __float_as_uint(-z.m[n][1]));
+    const uint64_t negm = pack2(__float_as_uint(-z.m[n][0]), __float_as_uint(-z.m[n][1])), lift = pair_f32(kLift);
 #pragma unroll
     for (int x = 0; x < X; ++x)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float p0, p1;
-        unpack2(mul2(add2(pack2(__float_as_uint(s[x][n][2 * i]), __float_as_uint(s[x][n][2 * i + 1])), negm), f2), p0, p1);
+        unpack2(fma2(add2(pack2(__float_as_uint(s[x][n][2 * i]), __float_as_uint(s[x][n][2 * i + 1])), negm), f2, lift),
+                p0, p1);
         p0 = ex2(p0);
         p1 = ex2(p1);
         z.l[n] = add2(z.l[n], pack2(__float_as_uint(p0), __float_as_uint(p1)));
@@ -463,12 +469,12 @@ __device__ __forceinline__ void init_smem(Smem<D>& sm, int warp, int lane) {
   if (threadIdx.x == 0) sm.abort_flag = 0;
 }
 
-// What a weight is made of again: 2^((product - maximum) factor) / sum. Maxima are
+// What a weight is made of again: 2^((product - maximum) factor) / sum, with the sum's lift. Maxima are
 // joined and kept as products: a rounded maximum in log2 units would be off by
 // 2^-24 of itself, and the log of the sum lost beside it, which counts from logits
 // of some 10^3 on and makes equal places of large ones weigh 1 each.
 __device__ __forceinline__ float2 row_stats(float top, float sum) {
-  return make_float2(top, sum == 0.0f ? 0.0f : 1.0f / sum);
+  return make_float2(top, sum == 0.0f ? 0.0f : static_cast<float>(1 << static_cast<int>(kLift)) / sum);
 }
 
 template <int D, int NT>
