@@ -430,7 +430,8 @@ VLM_API int vlm_expand_placeholders(const int64_t* d_input_ids, int64_t n_ids, i
  *   reach it, infinities and NaN included; a NaN logit makes its row NaN. An
  *   infinite value whose weight rounds to 0 gives its row that infinity or NaN,
  *   by its place, alike in every call.
- *   scale > 0. P is rounded to dtype, sums are fp32. A sequence's rows do not
+ *   scale > 0. P is rounded to dtype (fp16: below 2^-21 of the row's largest
+ *   weight to within 2^-32 of it), sums are fp32. A sequence's rows do not
  *   depend on the other sequences. No workspace; d_out must not overlap k and
  *   v. d_status may be NULL here and in the vlm_kv4_* calls (device-side errors
  *   then go unreported).

@@ -83,3 +83,25 @@ def test_many_small_weights_beside_a_large_one(dim, dtype, gap):
     e = 2.0 ** -11 + 2 * (gap * 5 * 2.0 ** -24 + 2.0 ** -21) + 2 * (n // 4) * 2.0 ** -24
     tol = u * np.abs(o) + e * a * (1 + u) + 2.0 ** -32 * n * 24 * V_SG + float(torch.finfo(dtype).smallest_normal) * u
     U.assert_close(got, np.broadcast_to(o, got.shape), np.broadcast_to(tol, got.shape))
+
+
+@pytest.mark.parametrize("gap", [20.6, 25.5])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_many_small_weights_beside_a_large_one_in_a_prompt(dtype, dim, gap):
+    # 131,072 keys, the first with 2^gap times the others' weight and a value of 0: the others are the whole output
+    n, m = 131072, 3
+    q, k = torch.zeros((m, 2, dim), dtype=dtype), torch.zeros((n, 1, dim), dtype=dtype)
+    q[..., 0], k[0, 0, 0] = 1.0, 8.0
+    v = U.rand16(51, (n, 1, dim), dtype).abs()
+    v[0] = 0
+    scale = float(np.float32(gap * np.log(2.0) / 8.0))
+    o, a = T.prompt_attention(q.float().numpy(), k.float().numpy(), v.float().numpy(), [m], [n], scale)
+    got = vlm.prompt_attention(q.cuda(), k.cuda(), v.cuda(), [m], [n], scale=scale)
+    # P rounded (half a step; fp16's weights under 2^-21 of the largest by 2^-32 of it), exponentials of exact logits
+    # (scale log2 e, the maximum's and the difference's products rounded: 2^-24 of them each; the unit 2^-21), fp32
+    # sums of 1,024 tiles of 64 keys in O and in the row's sum, the tensor core's truncated to 2^-23
+    u = U.half_step(dtype)
+    e = u + 2 * (gap * 4 * 2.0 ** -24 + 2.0 ** -21) + (1024 + 64) * 2.0 ** -24 + 1024 * 8 * 2.0 ** -23
+    floor = 2.0 ** -32 * n * float(v.max()) if dtype == torch.float16 else 0.0
+    U.assert_close(got, o, u * np.abs(o) + e * a * (1 + u) + floor + float(torch.finfo(dtype).smallest_normal) * u)

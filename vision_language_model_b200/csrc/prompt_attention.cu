@@ -46,8 +46,9 @@
 // S for registers at once, so the buffer is free again while its softmax runs.
 // D = 64: S [0, 128) and [128, 256), P [256, 384), O [384, 512).
 //
-// Roundings: P to the inputs' type (half a step; P <= 2^8 and its fp32 sum is
-// taken before rounding), the output once; everything else is fp32.
+// Roundings: P to the inputs' type (half a step; fp16 weights, which are made 2^7
+// times as large, below 2^-21 of the row's largest to within 2^-32 of it; its fp32
+// sum is taken before rounding), the output once; everything else is fp32.
 // Places that a row does not see get weight 0. A weight of 0 does not stop an
 // infinity or NaN in V, so on key tiles that some row of the item does not see in
 // full the softmax threads of both row tiles look V over in shared memory before
@@ -540,13 +541,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           l *= corr;
           ref = m == -INFINITY ? 0.0f : m;
           // Logits of ordinary size: 2^(s sl2 - m sl2) in one operation; the rounding of
-          // m sl2 scales the row's weights by up to 2^(2^-13) alike. Masked tiles and
-          // large logits are subtracted before they are scaled. (Rows without a token do
-          // not vote: they hold other sequences' queries or nothing.)
-          large = __any_sync(0xffffffffu, live && fabsf(ref * args.sl2) > 4096.0f);
+          // m sl2 (less fp16's lift) scales the row's weights by up to 2^(2^-13) alike.
+          // Masked tiles and large logits are subtracted before they are scaled. (Rows
+          // without a token do not vote: they hold other sequences' queries or nothing.)
+          large = __any_sync(0xffffffffu, live && fabsf(ref * args.sl2) > 4096.0f - kHalfLift);
         }
         uint32_t pk[HK / 2];
-        l += !masked && !large ? row_exp<false, kHalf>(u, sl2x2, ref * args.sl2, pk)
+        l += !masked && !large ? row_exp<false, kHalf>(u, sl2x2, fmaf(ref, args.sl2, kHalf ? -kHalfLift : 0.0f), pk)
                                : row_exp<false, kHalf, true>(u, sl2x2, ref, pk);
         if (j > 0) {
           // the product with the tile before must be done before O is rescaled and P overwritten

@@ -114,10 +114,17 @@ __device__ __forceinline__ float exp2_poly(float x) {
   return __int_as_float(__float_as_int(p) + (__float_as_int(j) << 23));
 }
 
+// Log2 units that fp16 weights are larger by, and their sums with them: they stay
+// below 2^8 of their maximum, so this fills fp16's largest powers of two and takes
+// the weights that it holds in 11 bits down from 2^-14 to 2^-21 of the maximum, the
+// smallest that it tells from 0 from 2^-25 to 2^-32.
+constexpr float kHalfLift = 7.0f;
+
 // p_c = 2^(s_c * sl2 - m) for the thread's N scores of the row, packed as pairs (bf16,
 // or fp16 with kHalf) into pk; returns sum_c p_c (fp32, before rounding). The elements are independent.
-// kRaw: m is in the scores' own units and p_c = 2^((s_c - m) * sl2), one more
-// operation per pair, for scores of any size: a product rounded before it is
+// With kHalf the caller takes kHalfLift from m.
+// kRaw: m is in the scores' own units and p_c = 2^((s_c - m) * sl2) (with kHalf
+// lifted here), one more operation per pair, for scores of any size: a product rounded before it is
 // subtracted would be off by 2^-24 of itself, which counts from some 10^8 on.
 // kPoly: let exp2_poly take one pair in kPolyPairEvery (never on a tile with
 // masked keys, whose weights must be exactly 0).
@@ -128,8 +135,12 @@ __device__ __forceinline__ float row_exp(const uint32_t (&u)[N], uint64_t sl2x2,
 #pragma unroll
   for (int c = 0; c < N; c += 2) {
     float x0, x1, p0, p1;
-    unpack2(kRaw ? mul2(add2(pack2(u[c], u[c + 1]), negm2), sl2x2) : fma2(pack2(u[c], u[c + 1]), sl2x2, negm2), x0,
-            x1);
+    if (kRaw) {
+      const uint64_t d = add2(pack2(u[c], u[c + 1]), negm2);
+      unpack2(kHalf ? fma2(d, sl2x2, pair_f32(kHalfLift)) : mul2(d, sl2x2), x0, x1);
+    } else {
+      unpack2(fma2(pack2(u[c], u[c + 1]), sl2x2, negm2), x0, x1);
+    }
     if (kPoly && kPolyPairEvery > 0 && (c >> 1) % (kPolyPairEvery > 0 ? kPolyPairEvery : 1) == kPolyPairEvery - 1) {
       p0 = exp2_poly(x0);
       p1 = exp2_poly(x1);
