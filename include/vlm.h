@@ -526,7 +526,8 @@ VLM_API int vlm_kv4_read(const vlm_kv4_cache* cache, const int32_t* d_table, int
  *   weights, 0 behind them.
  * d_kept: NULL, or int32 [n_seqs][kv_heads][budget]: the kept places, -1
  *   behind them.
- * The results must not overlap d_lens and d_weights (VLM_ERR_INVALID_ARG).
+ * The results must overlap neither each other nor any other buffer of the call
+ * (VLM_ERR_INVALID_ARG).
  * d_workspace: 256-byte aligned, vlm_kv4_evict_workspace_size bytes.
  * ------------------------------------------------------------------------- */
 VLM_API size_t vlm_kv4_attention_workspace_size(int n_seqs, int heads, int kv_heads, int head_dim, int q_len);

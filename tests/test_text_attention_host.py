@@ -175,3 +175,19 @@ def test_tables_whose_places_leave_no_room_in_32_bits_are_refused(L, call):
         assert _evict(L, to_width=room + 1, n=1) == vlm.ERR_BAD_SHAPE
     # as many entries in all as 32-bit offsets of the sequences take, two more each
     assert call(L, width=(2 ** 31 - 1) // 64, n=64) == vlm.ERR_BAD_SHAPE
+
+
+@pytest.mark.parametrize("kw", [
+    dict(kept=A + 512), dict(kept=C), dict(kept=C - 1532), dict(kept=B), dict(kept=E), dict(kept=C + 4096), dict(kept=6 << 20),
+    dict(to_lens=A + 4), dict(to_lens=C), dict(to_lens=B + 44), dict(to_lens=E), dict(to_lens=(6 << 20) + 64),
+    dict(to_weights=C), dict(to_weights=C - 4), dict(to_weights=B - 8), dict(to_weights=E - 1532), dict(to_weights=7 << 20),
+    dict(to_weights=C + 4100),
+    dict(kept=None, to_lens=A),
+    dict(weights=9 << 20, ws=8 << 20, to_weights=A + (180 << 10) - 8),  # over the pool's last page
+    dict(weights=9 << 20, ws=8 << 20, kept=(8 << 20) + 64),          # over the workspace
+])
+def test_eviction_refuses_results_over_other_buffers(L, kw):
+    # kernels write the results while other CTAs still read what the call was given
+    before = vlm.launch_count()
+    assert _evict(L, **kw) == vlm.ERR_INVALID_ARG, kw
+    assert vlm.launch_count() == before

@@ -185,13 +185,30 @@ int vlm_kv4_evict(const vlm_kv4_cache* cache, const int32_t* d_table, int max_pa
   if (to_max_pages <= 0 || to_max_pages > kMaxPages || budget > to_max_pages * kKv4Page ||
       static_cast<int64_t>(to_max_pages) * n_seqs > INT_MAX)
     return VLM_ERR_BAD_SHAPE;
-  // results over the inputs that other CTAs still read
+  // results over what other CTAs still read, or over one another
   const size_t units = static_cast<size_t>(n_seqs) * cache->kv_heads;
-  if (overlap(d_lens, n_seqs * 4ull, d_to_lens, n_seqs * 4ull) ||
-      overlap(d_weights, units * max_pages * kKv4Page * 4, d_to_weights, units * to_max_pages * kKv4Page * 4))
-    return VLM_ERR_INVALID_ARG;
-  if (ws_bytes < vlm_kv4_evict_workspace_size(cache->n_pages, n_seqs, cache->kv_heads, budget))
-    return VLM_ERR_WORKSPACE;
+  const size_t need = vlm_kv4_evict_workspace_size(cache->n_pages, n_seqs, cache->kv_heads, budget);
+  struct Span {
+    const void* p;
+    size_t n;
+  };
+  const Span results[] = {{d_to_lens, n_seqs * 4ull},
+                          {d_to_weights, units * to_max_pages * kKv4Page * 4},
+                          {d_kept, d_kept == nullptr ? 0 : units * budget * 4}};
+  const Span others[] = {{d_lens, n_seqs * 4ull},
+                         {d_weights, units * max_pages * kKv4Page * 4},
+                         {d_table, static_cast<size_t>(n_seqs) * max_pages * 4},
+                         {d_to_table, static_cast<size_t>(n_seqs) * to_max_pages * 4},
+                         {c.pages, static_cast<size_t>(c.n_pages) * cache->kv_heads * kv4_head_bytes(cache->head_dim)},
+                         {d_workspace, need}};
+  for (int i = 0; i < 3; ++i) {
+    if (results[i].n == 0) continue;
+    for (const Span& o : others)
+      if (overlap(results[i].p, results[i].n, o.p, o.n)) return VLM_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(results[i].p, results[i].n, results[j].p, results[j].n)) return VLM_ERR_INVALID_ARG;
+  }
+  if (ws_bytes < need) return VLM_ERR_WORKSPACE;
   return launch_kv4_evict(c, cache->head_dim, d_weights, budget, sinks, recent, d_to_table, to_max_pages, d_to_lens,
                           d_to_weights, d_kept, d_workspace, d_status, as_stream(stream));
 }
