@@ -427,7 +427,8 @@ VLM_API int vlm_expand_placeholders(const int64_t* d_input_ids, int64_t n_ids, i
  *   kv_len > q_len is a prompt that goes on (its first keys from a cache); a
  *   query that sees no key (kv_len < q_len) gives 0. Only the rows of the
  *   listed queries are written. Keys and values that a row does not see do not
- *   reach it, infinities and NaN included; a NaN logit makes its row NaN. An
+ *   reach it, infinities and NaN included; a NaN logit makes its row NaN, as
+ *   do logits that are all -infinity. An
  *   infinite value whose weight rounds to 0 gives its row that infinity or NaN,
  *   by its place, alike in every call.
  *   scale > 0. P is rounded to dtype (fp16: below 2^-21 of the row's largest
@@ -496,7 +497,8 @@ VLM_API int vlm_kv4_read(const vlm_kv4_cache* cache, const int32_t* d_table, int
  *
  * d_lens: device int32 [n_seqs], tokens in the cache, the new ones included.
  *   New token i sits at place len - q_len + i and sees the places up to its
- *   own; without any (len 0, or a place before 0) its row is 0. Sums are fp32;
+ *   own; without any (len 0, or a place before 0) its row is 0. A row whose
+ *   logits are NaN or all -infinity (infinite queries) is NaN. Sums are fp32;
  *   a weight is rounded to 11 bits (below 2^-21 of its row's largest to within
  *   2^-32 of that), a query's values below 2^-14 of its largest to within 2^-25
  *   of that.

@@ -105,3 +105,39 @@ def test_many_small_weights_beside_a_large_one_in_a_prompt(dtype, dim, gap):
     e = u + 2 * (gap * 4 * 2.0 ** -24 + 2.0 ** -21) + (1024 + 64) * 2.0 ** -24 + 1024 * 8 * 2.0 ** -23
     floor = 2.0 ** -32 * n * float(v.max()) if dtype == torch.float16 else 0.0
     U.assert_close(got, o, u * np.abs(o) + e * a * (1 + u) + floor + float(torch.finfo(dtype).smallest_normal) * u)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_row_whose_logits_are_all_minus_infinity_is_nan(dim, dtype):
+    # the softmax of nothing but -inf is 0 / 0; only a query that sees no key at all gives 0
+    heads, kv_heads, q_lens, kv_lens = 4, 2, [200, 9], [200, 5]
+    q = U.rand16(61, (sum(q_lens), heads, dim), dtype)
+    k, v = (U.rand16(s, (sum(kv_lens), kv_heads, dim), dtype) for s in (62, 63))
+    q[..., 0] = q[..., 0].abs() + 0.5
+    k[:50, :, 0] = float("-inf")
+    scale = dim ** -0.5
+    got = vlm.prompt_attention(q.cuda(), k.cuda(), v.cuda(), q_lens, kv_lens)
+    o, a = T.prompt_attention(q.float().numpy(), k.float().numpy(), v.float().numpy(), q_lens, kv_lens, scale)
+    assert np.isnan(o[:50]).all() and torch.isnan(got[:50].float()).all()
+    ds = U.logit_error(q.float().numpy(), np.where(np.isfinite(k.float().numpy()), k.float().numpy(), 0.0), scale)
+    U.assert_close(got[50:], o[50:], U.prompt_tolerance(dtype, o[50:], a[50:], ds))
+    assert not got[200:204].any()
+
+
+@pytest.mark.parametrize("width", [128, 140])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_cache_row_whose_logits_are_all_minus_infinity_is_nan(dim, width):
+    lens, heads, kv_heads = [70, 0, 300], 4, 2
+    pages, table, _ = U.random_pool(64, lens, kv_heads, dim, width=width)
+    at, n, w = T._parts(dim)[0]
+    pages[..., at:at + n:w] |= 0x0F  # column 0 of every key: -6
+    q = U.rand16(65, (len(lens) * 2, heads, dim), torch.bfloat16)
+    q[:, 1, 0] = float("inf")
+    gw = torch.zeros((len(lens), kv_heads, width * PAGE), device="cuda")
+    got = vlm.kv4_attention(guarded_copy(torch.from_numpy(pages)), U.cuda_int(table), U.cuda_int(lens), guarded_copy(q),
+                            K_SG, V_SG, weights=gw).float().cpu()
+    o, _, want = T.cache_attention(pages, table, lens, q.float().numpy(), 2, K_SG, V_SG, dim ** -0.5)
+    assert np.array_equal(np.isnan(o), torch.isnan(got).numpy())
+    assert torch.isnan(got[:2, 1]).all() and torch.isnan(got[4:, 1]).all() and not got[2:4].any()
+    assert np.array_equal(np.isnan(want), torch.isnan(gw).cpu().numpy())

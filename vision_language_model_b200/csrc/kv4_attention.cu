@@ -45,7 +45,7 @@
 // and token; they are made again from the keys.
 // Places behind what a row sees get logit -inf; value scales of places behind
 // the sequence's end are taken as 0, so stale bytes (NaN scales among them)
-// reach no sum. A row that sees nothing is 0.
+// reach no sum. A row that sees nothing is 0, one whose logits are all -inf NaN.
 #include <cfloat>
 
 #include <algorithm>
@@ -474,7 +474,12 @@ __device__ __forceinline__ void init_smem(Smem<D>& sm, int warp, int lane) {
 // 2^-24 of itself, and the log of the sum lost beside it, which counts from logits
 // of some 10^3 on and makes equal places of large ones weigh 1 each.
 __device__ __forceinline__ float2 row_stats(float top, float sum) {
-  return make_float2(top, sum == 0.0f ? 0.0f : static_cast<float>(1 << static_cast<int>(kLift)) / sum);
+  return make_float2(top, static_cast<float>(1 << static_cast<int>(kLift)) / sum);
+}
+// What O is multiplied by. A sum of 0: no place seen, or logits that are all -inf, whose
+// softmax is 0 / 0 (and so are the weights).
+__device__ __forceinline__ float row_scale(float v_sg, float sum, int seen) {
+  return sum != 0.0f ? v_sg / sum : seen > 0 ? NAN : 0.0f;
 }
 
 template <int D, int NT>
@@ -603,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(const Ar
         if (row >= a.rows) continue;
         // columns g D / 8 + 2 j (elements r) and + 1 (elements 2 + r) of tile j
         if (whole) {
-          const float inv = l[r] == 0.0f ? 0.0f : a.c.v_sg / l[r];
+          const float inv = row_scale(a.c.v_sg, l[r], seen[n][r]);
           T* dst = static_cast<T*>(a.out) +
                    ((static_cast<int64_t>(at.s) * a.q_len + row / a.group) * a.heads + at.kvh * a.group + row % a.group) * D +
                    g * (D / 8);
@@ -838,7 +843,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, kCt
     if (cols) join[warp][lane] = t;
     __syncthreads();
     if (warp == 0) {
-      const float inv = sum == 0.0f ? 0.0f : a.c.v_sg / sum;
+      const float inv = row_scale(a.c.v_sg, sum, open + row / a.group);
       if (cols) {
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) {
@@ -966,7 +971,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_combine_kernel(const Args
       t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
     }
   }
-  const float inv = sum == 0.0f ? 0.0f : a.c.v_sg / sum;
+  const int seen = sum != 0.0f ? 0 : kv4_len(a.c, s, nullptr) - a.q_len + 1 + row / a.group;
+  const float inv = row_scale(a.c.v_sg, sum, seen);
   if (mine)
     store4<T>(static_cast<T*>(a.out) +
                   ((static_cast<int64_t>(s) * a.q_len + row / a.group) * a.heads + kvh * a.group + row % a.group) * D +

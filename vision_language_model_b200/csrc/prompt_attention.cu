@@ -628,7 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && n > 0) ok = mbar_wait_warp(smem_u32(o_done + t), (oc - 1) & 1, abort_v, args.status);
       if (ok) {
         tc_fence_after();
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        // a sum of 0: no key seen, or logits that are all -inf, whose softmax is 0 / 0
+        const float inv = l != 0.0f ? 1.0f / l : lim > 0 ? NAN : 0.0f;
         uint32_t noted = 0;
         if (n > 0) {
 #pragma unroll
