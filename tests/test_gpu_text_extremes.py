@@ -141,3 +141,25 @@ def test_a_cache_row_whose_logits_are_all_minus_infinity_is_nan(dim, width):
     assert np.array_equal(np.isnan(o), torch.isnan(got).numpy())
     assert torch.isnan(got[:2, 1]).all() and torch.isnan(got[4:, 1]).all() and not got[2:4].any()
     assert np.array_equal(np.isnan(want), torch.isnan(gw).cpu().numpy())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_infinite_values_reach_the_rows_that_see_them(dim, dtype):
+    heads, kv_heads, lens = 4, 2, [150, 90, 333]
+    n = sum(lens)
+    q, k, v = (U.rand16(s, (n, h, dim), dtype) for s, h in ((1, heads), (2, kv_heads), (3, kv_heads)))
+    at = 0
+    for m in lens:
+        for j, col, bad in ((100, 60, float("inf")), (130, 14, float("-inf")), (101, 3, float("nan"))):
+            if j < m:
+                v[at + j, :, col] = bad
+        at += m
+    got = vlm.prompt_attention(q.cuda(), k.cuda(), v.cuda(), lens).float().cpu()
+    at = 0
+    for m in lens:
+        x = got[at:at + m]
+        assert (x[100:, :, 60] == float("inf")).all() and torch.isfinite(x[:100]).all()
+        assert (x[130:, :, 14] == float("-inf")).all() and torch.isfinite(x[:130, :, 14]).all()
+        assert torch.isnan(x[101:, :, 3]).all() and torch.isfinite(x[:101, :, 3]).all()
+        at += m
