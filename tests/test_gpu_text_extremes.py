@@ -163,3 +163,26 @@ def test_infinite_values_reach_the_rows_that_see_them(dim, dtype):
         assert (x[130:, :, 14] == float("-inf")).all() and torch.isfinite(x[:130, :, 14]).all()
         assert torch.isnan(x[101:, :, 3]).all() and torch.isfinite(x[:101, :, 3]).all()
         at += m
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("q_lens,kv_lens,heads,kv_heads,dim", [
+    ([300], [300], 8, 2, 128), ([300], [300], 8, 2, 64), ([70, 1, 129], [500, 130, 129], 6, 2, 64), ([257], [300], 3, 3, 128),
+])
+def test_a_prompt_with_exact_logits_is_off_by_its_roundings_alone(q_lens, kv_lens, heads, kv_heads, dim, dtype):
+    # one column per query is not 0, so a logit is one product of two 16-bit values, exact in fp32
+    T_ = sum(q_lens)
+    g = torch.Generator().manual_seed(91)
+    hot = torch.nn.functional.one_hot(torch.randint(0, dim, (T_, heads), generator=g), dim)
+    q = (U.rand16(92, (T_, heads, dim), torch.float32) * 6.0 * hot).to(dtype)
+    k, v = (U.rand16(s, (sum(kv_lens), kv_heads, dim), dtype) for s in (93, 94))
+    scale = 0.5
+    o, a = T.prompt_attention(q.float().numpy(), k.float().numpy(), v.float().numpy(), q_lens, kv_lens, scale)
+    got = vlm.prompt_attention(q.cuda(), k.cuda(), v.cuda(), q_lens, kv_lens, scale=scale)
+    # logits up to L in log2 units: the scale, the maximum's and the exponent's products round them by 2^-24 each; the
+    # unit 2^-21; both in the weights and in their sum. The tensor core truncates each of the n terms of a sum to 2^-23.
+    L = scale * 1.4427 * float(q.float().abs().max() * k.float().abs().max())
+    n, u = max(kv_lens), U.half_step(dtype)
+    e = u + 2 * (5 * L * 2.0 ** -24 + 2.0 ** -21) + n * (2.0 ** -23 + 2.0 ** -24)
+    floor = 2.0 ** -32 * n * float(v.float().abs().max()) if dtype == torch.float16 else 0.0
+    U.assert_close(got, o, u * np.abs(o) + e * a * (1 + u) + floor + float(torch.finfo(dtype).smallest_normal) * u)
