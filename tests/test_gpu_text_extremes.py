@@ -186,3 +186,23 @@ def test_a_prompt_with_exact_logits_is_off_by_its_roundings_alone(q_lens, kv_len
     e = u + 2 * (5 * L * 2.0 ** -24 + 2.0 ** -21) + n * (2.0 ** -23 + 2.0 ** -24)
     floor = 2.0 ** -32 * n * float(v.float().abs().max()) if dtype == torch.float16 else 0.0
     U.assert_close(got, o, u * np.abs(o) + e * a * (1 + u) + floor + float(torch.finfo(dtype).smallest_normal) * u)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_scales_up_to_the_largest_fp32_value(dim):
+    # the key whose product is largest has all the weight, however large the logits get
+    heads, kv_heads, n = 4, 2, 150
+    q, k, v = (U.rand16(s, (n, h, dim), torch.bfloat16) for s, h in ((95, heads), (96, kv_heads), (97, kv_heads)))
+    o, _ = T.prompt_attention(q.float().numpy(), k.float().numpy(), v.float().numpy(), [n], [n], 3e38)
+    got = vlm.prompt_attention(q.cuda(), k.cuda(), v.cuda(), [n], scale=3e38)
+    U.assert_close(got, o, 2.0 ** -8 * np.abs(o) + 1e-30)
+    lens = [150, 65]
+    pages, table, _ = U.random_pool(98, lens, kv_heads, dim)
+    cq = U.rand16(99, (2, heads, dim), torch.bfloat16, 2.0 ** 120)
+    for k_sg, scale in ((K_SG, 3e38), (3e38, 1.0)):
+        o, _, w = T.cache_attention(pages, table, lens, cq.float().numpy(), 1, k_sg, V_SG, scale)
+        gw = torch.zeros((2, kv_heads, table.shape[1] * PAGE), device="cuda")
+        got = vlm.kv4_attention(guarded_copy(torch.from_numpy(pages)), U.cuda_int(table), U.cuda_int(lens), cq.cuda(), k_sg,
+                                V_SG, scale=scale, weights=gw)
+        U.assert_close(got, o, 2.0 ** -8 * np.abs(o) + 1e-30)
+        assert np.array_equal(gw.cpu().numpy(), w.astype(np.float32))

@@ -198,7 +198,8 @@ __device__ __forceinline__ void load_q(const Args& a, int s, int kvh, int first,
     // 2^-floor(log2 amax); 1 where amax is 0, subnormal or infinite
     const int e = static_cast<int>(__float_as_uint(amax) >> 23);
     const float mul = e == 0 || e == 255 ? 1.0f : __uint_as_float(static_cast<uint32_t>(max(254 - e, 1)) << 23);
-    const float mine = fmaxf(a.scale * a.c.k_sg * kLog2e / mul, FLT_MIN);  // not 0: it multiplies -inf
+    // not 0 and not infinite: it multiplies -inf and differences of 0
+    const float mine = fminf(fmaxf(a.scale * a.c.k_sg * kLog2e / mul, FLT_MIN), FLT_MAX);
     factor[n][0] = __shfl_sync(0xffffffffu, mine, 8 * c);
     factor[n][1] = __shfl_sync(0xffffffffu, mine, 8 * c + 4);
 #pragma unroll

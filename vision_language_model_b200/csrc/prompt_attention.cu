@@ -58,6 +58,7 @@
 // row's weight rounds to 0.)
 // A query that sees no key (kv_len < q_len) gives 0.
 #include <algorithm>
+#include <cfloat>
 #include <functional>
 #include <numeric>
 #include <vector>
@@ -876,7 +877,7 @@ int launch_prompt_attention(const PromptAttn& p, cudaStream_t s) {
       a.kv_heads = p.kv_heads;
       a.group = group;
       a.tpt = tpt;
-      a.sl2 = p.scale * 1.4426950408889634f;
+      a.sl2 = std::min(p.scale * 1.4426950408889634f, FLT_MAX);  // not infinite: it multiplies differences of 0
       a.v = p.v;
       a.v_stride = p.v_stride;
       a.out = p.out;
