@@ -360,7 +360,7 @@ def ncu_traffic(kernel: str) -> float | None:
     return float(ent["bytes_per_launch"])
 
 
-KERNEL_SOURCES = {"attention": ["attention_tc.cu", "exp2_poly.cuh", "common.cuh", "kernels.cuh"],
+KERNEL_SOURCES = {"attention": ["attention_tc.cu", "softmax.cuh", "exp2_poly.cuh", "common.cuh", "kernels.cuh"],
                   "gemm": ["gemm_tcgen05.cu", "common.cuh", "kernels.cuh"],
                   "resize": ["frontend.cu", "common.cuh", "kernels.cuh"]}
 

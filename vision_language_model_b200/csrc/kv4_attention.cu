@@ -37,12 +37,12 @@
 //     A unit (sequence, key head, row tile) cut by a border leaves partial sums
 //     that kv4_combine_kernel joins in the order of the runs: the result does
 //     not depend on timing (its last bits do on where the batch was cut).
-// Measured, 32/8 heads of 128: 31 sequences of up to 16,000 tokens (378 MB) 76 us,
-// of which the join is 4 to 5; three of 131,072 (452 MB) 85 us, 5.3 TB/s (0.81 of
-// the copy rate). What it lacks is issue slots, 58% used, 430 instructions per 32
-// tokens of a head of which 256 convert and scale. As 16-row tiles of S and O it
-// took 104 us. For the weights, logits stored in fp32 would cost 8 bytes per row
-// and token; they are made again from the keys.
+// Measured (a graph of the call replayed), 32/8 heads of 128: 31 sequences of up to
+// 16,000 tokens (378 MB) 74 us, of which the join is 4 to 5; 131,072, 131,071, 98,304
+// and 77 (415 MB) 80 us, 5.2 TB/s (0.79 of the copy rate). What it lacks is issue
+// slots, 58% used, 430 instructions per 32 tokens of a head of which 256 convert and
+// scale. As 16-row tiles of S and O it took 104 us. For the weights, logits stored in
+// fp32 would cost 8 bytes per row and token; they are made again from the keys.
 // Places behind what a row sees get logit -inf; value scales of places behind
 // the sequence's end are taken as 0, so stale bytes (NaN scales among them)
 // reach no sum. A row that sees nothing is 0, one whose logits are all -inf NaN.
@@ -60,7 +60,10 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxSeqs = 4096;  // sequences per launch (their page offsets are held in shared memory)
-constexpr int kCtasPerSm = 3;  // 168 registers; four CTAs would have to spill
+// 168 registers; four CTAs would have to spill. Three also have room for the offsets of some
+// 740 sequences in their shared memory (by clusters of 90); with more in a launch two are
+// resident, and the last third of the grid follows them.
+constexpr int kCtasPerSm = 3;
 constexpr int kCluster = 8;       // CTAs that share a unit of a small batch
 constexpr int kClusterPages = 128;  // and the pages a sequence may then have: four per warp
 constexpr int kMinPages = 1;  // of a run: a page takes a warp about 1 us, joining a run less
@@ -1135,7 +1138,8 @@ int launch_kv4_attention(const Kv4& c0, int head_dim, int heads, int q_len, int 
   // A small batch goes by clusters, no warp with more than a few pages: where all units'
   // clusters run at once, or in two waves if the weights are wanted too, which the cluster
   // takes from the pages that it has at hand (one row tile), and the table has a page for
-  // every warp. By runs against by clusters, heads of 128, group 4: one sequence of 3,242
+  // every warp. The table's width stands in for the lengths, which only the device knows: a
+  // wider table goes by runs however short its sequences are. By runs against by clusters, heads of 128, group 4: one sequence of 3,242
   // places, 8 key heads, 12.6 and 8.5 us; 12 of up to 4,000, 4 key heads (48 units), 18.5
   // and 12.4; 8 of up to 8,000, 8 key heads (64 units), 22.7 and 24.8. With weights, 4
   // tokens: 24 of up to 4,000, 4 key heads (96 units), 50.8 and 45.2; of 500 places, 26.7

@@ -32,12 +32,15 @@
 // copied (250 cycles), handed over (350), S_1's product runs (512) and is
 // reported (430): about 3,000 cycles per key tile against the tensor core's
 // 2,048 and the exponential unit's 1,800. Handing S over in halves of 64 keys
-// (N = 64 products) was slower. D = 64: the softmax itself, 2,500 cycles per key
+// (N = 64 products) was slower; P over its own S, which would leave each row tile a
+// buffer of its own, is not built. D = 64: the softmax itself, 2,500 cycles per key
 // tile. An item costs 5,000 to 9,000 cycles besides: its last product, O to memory,
-// and the look at V below. Measured, 32/8 heads of 128, bf16: 4,096 tokens 112
-// to 118 us, 1,170 to 1,230 TFLOP/s (0.71 to 0.75 of the measured peak, by the box);
-// 8,192 tokens 411 to 425 us, 1,290 to 1,340; 3,241 tokens 74 to 83 us;
-// heads of 64: 8,192 tokens 367 to 383 us, 720 to 740. The softmax's instructions
+// and the look at V below. Measured, one call replayed on the same inputs, 32/8 heads of
+// 128, bf16: 4,096 tokens 112 to 118 us, 1,170 to 1,230 TFLOP/s (0.71 to 0.75 of the
+// measured peak, by the box); 8,192 tokens 411 to 425 us, 1,290 to 1,340; 3,241 tokens
+// 74 to 83 us; four of 4,096 465 us, 1,180; heads of 64: 8,192 tokens 367 to 383 us,
+// 720 to 740. Passes over several sets of inputs in turn run into the power cap: 3,241
+// tokens 90 us, 955 TFLOP/s; four of 4,096 541 us, 1,020. The softmax's instructions
 // count as well, 57% of the issue slots: exponentials from polynomials beside
 // the unit (2% slower), maxima exchanged on every tile instead of where one
 // moves and a vote on the logits' size per tile (5% together) went for that.
