@@ -904,7 +904,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_combine_kernel(const Args
   griddep_launch_dependents();
   constexpr int kJoinThreads = kJoinWarps * 32;
   __shared__ float sm_o[kJoinWarps][D];
-  __shared__ float factor[kJoinThreads];
+  __shared__ float factor[kJoinThreads], row_factor;
   __shared__ float sm_red[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.y, tile = row / a.tile_rows, r = row % a.tile_rows;
@@ -925,20 +925,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_combine_kernel(const Args
   auto at = [&](int i) {
     return (2 * static_cast<int64_t>(i) + (i * chunk >= lo ? 0 : 1)) * a.tile_rows + r;
   };
-  const float scale = a.part_ml[at(i0)].z;  // the row's, in every part
   float top = -INFINITY, sum = 0.0f;
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
   const bool mine = lane * 4 < D;
   for (int base = i0; base <= i1; base += kJoinThreads) {  // as a rule once
     const int n = min(kJoinThreads, i1 - base + 1);
-    float2 ml = make_float2(-INFINITY, 0.0f);
-    if (static_cast<int>(threadIdx.x) < n) ml = *reinterpret_cast<const float2*>(a.part_ml + at(base + threadIdx.x));
+    float4 ml = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+    if (static_cast<int>(threadIdx.x) < n) ml = a.part_ml[at(base + threadIdx.x)];
     float m = ml.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     __syncthreads();
     if (lane == 0) sm_red[warp] = m;
+    if (threadIdx.x == 0) row_factor = ml.z;  // the same in every part
     __syncthreads();
+    const float scale = row_factor;
     m = top;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, sm_red[w]);
