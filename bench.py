@@ -360,8 +360,10 @@ def ncu_traffic(kernel: str) -> float | None:
     return float(ent["bytes_per_launch"])
 
 
-KERNEL_SOURCES = {"attention": ["attention_tc.cu", "softmax.cuh", "exp2_poly.cuh", "common.cuh", "kernels.cuh"],
-                  "gemm": ["gemm_tcgen05.cu", "common.cuh", "kernels.cuh"],
+# What a kernel is made of: its file and every header that it includes, so that a change to one of them voids the entry.
+KERNEL_SOURCES = {"attention": ["attention_tc.cu", "softmax.cuh", "exp2_poly.cuh", "nvfp4.cuh", "common.cuh", "kernels.cuh"],
+                  "gemm": ["gemm_tcgen05.cu", "gemm_rows.cuh", "nvfp4.cuh", "common.cuh", "kernels.cuh"],
+                  "rmsnorm": ["small_kernels.cu", "gemm_rows.cuh", "nvfp4.cuh", "common.cuh", "kernels.cuh"],
                   "resize": ["frontend.cu", "common.cuh", "kernels.cuh"]}
 
 
