@@ -182,7 +182,7 @@ def test_tables_whose_places_leave_no_room_in_32_bits_are_refused(L, call):
     dict(to_lens=A + 4), dict(to_lens=C), dict(to_lens=B + 44), dict(to_lens=E), dict(to_lens=(6 << 20) + 64),
     dict(to_weights=C), dict(to_weights=C - 4), dict(to_weights=B - 8), dict(to_weights=E - 1532), dict(to_weights=7 << 20),
     dict(to_weights=C + 4100),
-    dict(kept=None, to_lens=A),
+    dict(kept=None, to_lens=A), dict(to_lens=STATUS - 8), dict(to_weights=STATUS - 1532),
     dict(weights=9 << 20, ws=8 << 20, to_weights=A + (180 << 10) - 8),  # over the pool's last page
     dict(weights=9 << 20, ws=8 << 20, kept=(8 << 20) + 64),          # over the workspace
 ])

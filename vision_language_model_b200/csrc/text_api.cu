@@ -200,7 +200,8 @@ int vlm_kv4_evict(const vlm_kv4_cache* cache, const int32_t* d_table, int max_pa
                          {d_table, static_cast<size_t>(n_seqs) * max_pages * 4},
                          {d_to_table, static_cast<size_t>(n_seqs) * to_max_pages * 4},
                          {c.pages, static_cast<size_t>(c.n_pages) * cache->kv_heads * kv4_head_bytes(cache->head_dim)},
-                         {d_workspace, need}};
+                         {d_workspace, need},
+                         {d_status, 4}};
   for (int i = 0; i < 3; ++i) {
     if (results[i].n == 0) continue;
     for (const Span& o : others)
