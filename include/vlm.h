@@ -427,10 +427,9 @@ VLM_API int vlm_expand_placeholders(const int64_t* d_input_ids, int64_t n_ids, i
  *   kv_len > q_len is a prompt that goes on (its first keys from a cache); a
  *   query that sees no key (kv_len < q_len) gives 0. Only the rows of the
  *   listed queries are written. Keys and values that a row does not see do not
- *   reach it, infinities and NaN included; a NaN logit makes its row NaN, as
- *   do logits that are all -infinity. An
- *   infinite value whose weight rounds to 0 gives its row that infinity or NaN,
- *   by its place, alike in every call.
+ *   reach it, infinities and NaN included; a NaN logit makes its row NaN, as do
+ *   logits that are all -infinity. An infinite value whose weight rounds to 0
+ *   gives its row that infinity or NaN, by its place, alike in every call.
  *   scale > 0. P is rounded to dtype (fp16: below 2^-21 of the row's largest
  *   weight to within 2^-32 of it), sums are fp32. A sequence's rows do not
  *   depend on the other sequences. No workspace; d_out must not overlap k and
